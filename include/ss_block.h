@@ -1,0 +1,167 @@
+/*
+ * ss_block.h -- C ABI of the operators around the head-wise selective scan
+ * (libss_scan.so, MI355X / gfx950).  Types, status codes and conventions
+ * (device pointers, caller's stream, no allocation, no synchronisation,
+ * arguments checked before anything is launched) are those of ss_scan.h.
+ *
+ * Three operators that a block runs one after another:
+ *   residual norm   r = residual + scale * x,  out = r / rms(r) * weight
+ *   head scan       a linear recurrence with one decay per head and step and a
+ *                   (P, N) state per head, B and C shared by the heads of a group
+ *   gated norm      out = v / rms(v) * weight with v = y * silu(z), per group
+ * each with its backward pass, and the head scan with its single-token step.
+ *
+ * Head scan.  For batch b, head h of group g = h / (H / G), time t:
+ *     delta' = softplus(delta[b,t,h] + bias[h])        (or delta + bias)
+ *     a      = exp(delta' * A[h]),  A = -exp(A_log[h])
+ *     S      = a * S + delta' * x[b,t,h,:] B[b,t,g,:]^T          (P x N, fp32)
+ *     y      = S C[b,t,g,:] + D[h] * x[b,t,h,:]
+ * A step's decay below 2^-200 is taken as 2^-200 (both are 0 in fp32).  Steps
+ * are taken 64 at a time by matrix products.  With bf16 inputs the products
+ * that carry the state, and the sums behind last_state and the gradients of
+ * the fp32 parameters, are exact to fp32; the others round one operand to bf16
+ * and sum in fp32.
+ */
+#ifndef SS_BLOCK_H
+#define SS_BLOCK_H
+
+#include "ss_scan.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* Largest state size N of the head scan. */
+#define SS_MAX_HEAD_STATE 128
+/* Largest head size P of the head scan. */
+#define SS_MAX_HEAD_DIM 1024
+/* Most channels that a norm takes together. */
+#define SS_MAX_NORM_CHANNELS 16384
+
+/*
+ * Bytes of device workspace of ss_head_scan_fwd and ss_head_scan_bwd (0 when
+ * none, and 0 for invalid arguments).  They depend on the arguments only.
+ */
+size_t ss_head_scan_fwd_workspace_bytes(int64_t b, int64_t L, int64_t H, int64_t P, int64_t N, int64_t G, int dtype);
+size_t ss_head_scan_bwd_workspace_bytes(int64_t b, int64_t L, int64_t H, int64_t P, int64_t N, int64_t G, int dtype);
+
+/*
+ * Head scan, forward.
+ *
+ *   x          : (b, L, H, P)  dtype
+ *   delta      : (b, L, H)     dtype
+ *   A_log, D   : (H)           fp32
+ *   B, C       : (b, L, G, N)  dtype; G divides H
+ *   delta_bias : (H)           fp32, or NULL
+ *   delta_softplus : nonzero -> softplus(delta + bias), zero -> delta + bias
+ *   initial_state  : (b, H, P, N) fp32, or NULL for zero; it may be the
+ *                    last_state buffer itself
+ *   y          : (b, L, H, P)  dtype, output, contiguous
+ *   last_state : (b, H, P, N)  fp32, output, or NULL
+ *   strides    : NULL for contiguous inputs, or 8 element counts: the batch and
+ *                time strides of x, delta, B and C, in that order (a token's own
+ *                elements are contiguous).  So x, B and C may be column ranges
+ *                of one projection's rows.  Each at least 0 (SS_ERR_SHAPE).
+ *   workspace  : ss_head_scan_fwd_workspace_bytes() bytes, 256-byte aligned; it
+ *                needs no initialisation.
+ * P <= SS_MAX_HEAD_DIM, N <= SS_MAX_HEAD_STATE (else SS_ERR_UNSUPPORTED),
+ * L < 2^31 - 1024, b * H * ceil(P / 64) * ceil(L / 64) < 2^24 and every tensor
+ * at most 2^46 elements (else SS_ERR_SHAPE).  A non-finite x, B, C or delta
+ * reaches only the outputs at and after its time step that depend on it.
+ * Results are the same bit for bit on every run.  Returns an ss_status.
+ */
+int ss_head_scan_fwd(const void *x, const void *delta, const float *A_log, const void *B, const void *C,
+                     const float *D, const float *delta_bias, int delta_softplus, const float *initial_state,
+                     void *y, float *last_state, int64_t b, int64_t L, int64_t H, int64_t P, int64_t N, int64_t G,
+                     int dtype, const int64_t *strides, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Gradient of ss_head_scan_fwd with respect to every input, from dy (b, L, H, P)
+ * dtype, contiguous, and dlast_state (b, H, P, N) fp32 or NULL (zero):
+ *   dx     (b, L, H, P), ddelta (b, L, H), dB, dC (b, L, G, N)   dtype, contiguous
+ *   dA_log, dD (H) fp32;  ddelta_bias (H) fp32 or NULL;  dinitial_state (b, H, P, N) fp32 or NULL
+ * The states at the chunks' bounds are formed again in the workspace.  Sums
+ * over heads, rows and time have a fixed order: the results are the same bit
+ * for bit on every run.  A non-finite input or dy reaches gradients of its
+ * own head and group only, but there within its 64-step chunk also those of
+ * steps that do not depend on it.  Arguments, sizes and errors otherwise as for
+ * ss_head_scan_fwd; no output may overlap an input, another output or the
+ * workspace (SS_ERR_ALIAS).
+ */
+int ss_head_scan_bwd(const void *x, const void *delta, const float *A_log, const void *B, const void *C,
+                     const float *D, const float *delta_bias, int delta_softplus, const float *initial_state,
+                     const void *dy, const float *dlast_state, void *dx, void *ddelta, float *dA_log, void *dB,
+                     void *dC, float *dD, float *ddelta_bias, float *dinitial_state, int64_t b, int64_t L,
+                     int64_t H, int64_t P, int64_t N, int64_t G, int dtype, const int64_t *strides,
+                     void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * One decode step of the head scan: state (b, H, P, N) fp32 is read and
+ * overwritten; x (b, H, P), dt (b, H), B, C (b, G, N) and y (b, H, P) dtype,
+ * contiguous; A_log, D, dt_bias as above.  Sizes: N <= SS_MAX_HEAD_STATE,
+ * b * H * P < 2^28.
+ */
+int ss_head_state_update(float *state, const void *x, const void *dt, const float *A_log, const void *B,
+                         const void *C, const float *D, const float *dt_bias, int dt_softplus, void *y,
+                         int64_t b, int64_t H, int64_t P, int64_t N, int64_t G, int dtype, void *stream);
+
+/*
+ * Residual norm, forward: r = residual + scale * x, stored in residual_out, and
+ * out = r / sqrt(mean(r^2) + eps) * weight of r as stored.
+ *   x            : rows of d elements, dtype, x_stride elements apart
+ *   residual     : (rows, d) of type res_dtype, or NULL (zero)
+ *   scale        : (d) fp32, or NULL (one)
+ *   weight       : (d) fp32
+ *   out          : (rows, d) dtype
+ *   residual_out : (rows, d) res_dtype; it may be the residual buffer itself
+ * res_dtype is dtype or SS_F32 (else SS_ERR_DTYPE).  d <= SS_MAX_NORM_CHANNELS
+ * (else SS_ERR_UNSUPPORTED), eps >= 0 and finite, x_stride >= d,
+ * rows < 2^31 (else SS_ERR_SHAPE).
+ */
+int ss_residual_norm_fwd(const void *x, const void *residual, const float *scale, const float *weight, void *out,
+                         void *residual_out, int64_t rows, int64_t d, double eps, int dtype, int res_dtype,
+                         int64_t x_stride, void *stream);
+
+/*
+ * Its gradient, from dout (rows, d) dtype, dresidual_out (rows, d) res_dtype or
+ * NULL (zero) and the forward's residual_out:
+ *   dx        : (rows, d) dtype
+ *   dresidual : (rows, d) res_dtype, or NULL when not wanted
+ *   dweight   : (d) fp32
+ *   dscale    : (d) fp32; scale, x and dscale are given together or not at all (SS_ERR_NULL)
+ * workspace: ss_residual_norm_bwd_workspace_bytes() bytes, 256-byte aligned.
+ * The sums over rows have a fixed order.
+ */
+size_t ss_residual_norm_bwd_workspace_bytes(int64_t rows, int64_t d);
+int ss_residual_norm_bwd(const void *dout, const void *dresidual_out, const void *residual_out, const void *x,
+                         const float *scale, const float *weight, void *dx, void *dresidual, float *dweight,
+                         float *dscale, int64_t rows, int64_t d, double eps, int dtype, int res_dtype,
+                         int64_t x_stride, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Gated norm, forward.  Each row's d channels are `groups` groups of d / groups
+ * (SS_ERR_SHAPE if that is not whole; at most SS_MAX_NORM_CHANNELS each), normalised apart:
+ *   norm_before_gate == 0: v = y * silu(z), out = v / sqrt(mean(v^2) + eps) * weight
+ *   norm_before_gate != 0: out = y / sqrt(mean(y^2) + eps) * weight * silu(z)
+ * y, z: rows of d elements, dtype, y_stride and z_stride elements apart; weight
+ * (d) fp32; out (rows, d) dtype.
+ */
+int ss_gated_norm_fwd(const void *y, const void *z, const float *weight, void *out, int64_t rows, int64_t d,
+                      int64_t groups, double eps, int norm_before_gate, int dtype, int64_t y_stride,
+                      int64_t z_stride, void *stream);
+
+/*
+ * Its gradient, from dout (rows, d) dtype: dy, dz (rows, d) dtype, contiguous,
+ * dweight (d) fp32.  workspace: ss_gated_norm_bwd_workspace_bytes() bytes,
+ * 256-byte aligned.
+ */
+size_t ss_gated_norm_bwd_workspace_bytes(int64_t rows, int64_t d, int64_t groups);
+int ss_gated_norm_bwd(const void *dout, const void *y, const void *z, const float *weight, void *dy, void *dz,
+                      float *dweight, int64_t rows, int64_t d, int64_t groups, double eps, int norm_before_gate,
+                      int dtype, int64_t y_stride, int64_t z_stride, void *workspace, size_t workspace_bytes,
+                      void *stream);
+
+#ifdef __cplusplus
+}
+#endif
+#endif /* SS_BLOCK_H */

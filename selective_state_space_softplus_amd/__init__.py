@@ -559,3 +559,7 @@ def selective_scan(u, delta, A_log, B, C, D, z=None, delta_bias=None, delta_soft
     """y of the scan, differentiable with respect to every tensor argument (torch autograd); zoh selects
     the zero-order-hold input term."""
     return _SelectiveScan.apply(u, delta, A_log, B, C, D, z, delta_bias, delta_softplus, initial_state, bool(zoh))
+
+
+from .block import (gated_norm, gated_norm_bwd, gated_norm_fwd, head_scan, head_scan_bwd, head_scan_fwd,  # noqa: E402
+                    head_state_update, residual_norm, residual_norm_bwd, residual_norm_fwd)

@@ -1,0 +1,428 @@
+"""The operators around the head-wise selective scan: its forward, gradient and decode step, and the norms
+before and after it.  A ctypes binding over the entry points of ``include/ss_block.h``; the arithmetic is in the
+library's HIP kernels.
+
+  head_scan_fwd(x, delta, A_log, B, C, D, delta_bias=None, delta_softplus=True, initial_state=None,
+                return_last_state=False)                                      -> y  or  (y, last_state)
+  head_scan_bwd(x, delta, A_log, B, C, D, dy, delta_bias=None, delta_softplus=True, initial_state=None,
+                dlast_state=None)                                             -> dict of gradients
+  head_scan(x, delta, A_log, B, C, D, delta_bias=None, delta_softplus=True, initial_state=None,
+            return_last_state=False)                                          -> differentiable (autograd)
+  head_state_update(state, x, dt, A_log, B, C, D, dt_bias=None, dt_softplus=True)  -> y (state in place)
+  residual_norm_fwd(x, weight, residual=None, scale=None, eps=1e-5)           -> (out, residual_out)
+  residual_norm_bwd(dout, residual_out, weight, dresidual_out=None, x=None, scale=None, eps=1e-5)  -> dict
+  residual_norm(x, weight, residual=None, scale=None, eps=1e-5)               -> (out, residual_out), differentiable
+  gated_norm_fwd(y, z, weight, groups=1, eps=1e-5, norm_before_gate=False)    -> out
+  gated_norm_bwd(dout, y, z, weight, groups=1, eps=1e-5, norm_before_gate=False)  -> dict
+  gated_norm(y, z, weight, groups=1, eps=1e-5, norm_before_gate=False)        -> out, differentiable
+
+Head scan shapes: x (b, L, H, P); delta (b, L, H); B, C (b, L, G, N) with G dividing H; A_log, D, delta_bias (H) fp32;
+states (b, H, P, N) fp32.  x, B and C (and delta) may be views with any batch and time strides as long as a token's own
+elements are contiguous: column ranges of one projection's output need no copies.  Norms act on the last dimension.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from . import SS_BF16, SS_F32, SSError, _check, _dtype_code, _ptr, _stream, _workspace, lib
+
+SS_MAX_HEAD_STATE = 128
+SS_MAX_HEAD_DIM = 1024
+SS_MAX_NORM_CHANNELS = 16384
+EXPORTS = ("ss_head_scan_fwd", "ss_head_scan_fwd_workspace_bytes", "ss_head_scan_bwd",
+           "ss_head_scan_bwd_workspace_bytes", "ss_head_state_update", "ss_residual_norm_fwd", "ss_residual_norm_bwd",
+           "ss_residual_norm_bwd_workspace_bytes", "ss_gated_norm_fwd", "ss_gated_norm_bwd",
+           "ss_gated_norm_bwd_workspace_bytes")
+
+_P, _I64, _I, _SZ, _F64 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t, ctypes.c_double
+_SIGNATURES = {
+    "ss_head_scan_fwd_workspace_bytes": (_SZ, [_I64] * 6 + [_I]),
+    "ss_head_scan_bwd_workspace_bytes": (_SZ, [_I64] * 6 + [_I]),
+    "ss_head_scan_fwd": (_I, [_P] * 7 + [_I] + [_P] * 3 + [_I64] * 6 + [_I, _P, _P, _SZ, _P]),
+    "ss_head_scan_bwd": (_I, [_P] * 7 + [_I] + [_P] * 11 + [_I64] * 6 + [_I, _P, _P, _SZ, _P]),
+    "ss_head_state_update": (_I, [_P] * 8 + [_I, _P] + [_I64] * 5 + [_I, _P]),
+    "ss_residual_norm_fwd": (_I, [_P] * 6 + [_I64, _I64, _F64, _I, _I, _I64, _P]),
+    "ss_residual_norm_bwd_workspace_bytes": (_SZ, [_I64, _I64]),
+    "ss_residual_norm_bwd": (_I, [_P] * 10 + [_I64, _I64, _F64, _I, _I, _I64, _P, _SZ, _P]),
+    "ss_gated_norm_fwd": (_I, [_P] * 4 + [_I64, _I64, _I64, _F64, _I, _I, _I64, _I64, _P]),
+    "ss_gated_norm_bwd_workspace_bytes": (_SZ, [_I64] * 3),
+    "ss_gated_norm_bwd": (_I, [_P] * 7 + [_I64, _I64, _I64, _F64, _I, _I, _I64, _I64, _P, _SZ, _P]),
+}
+for _name, (_res, _args) in _SIGNATURES.items():
+    getattr(lib, _name).restype = _res
+    getattr(lib, _name).argtypes = _args
+
+
+def _check_tokens(t, name, shape, dtype, device):
+    """As _check, for a tensor (b, L, ...) whose batch and time strides are free."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    inner = 1
+    for size, stride in zip(reversed(t.shape[2:]), reversed(t.stride()[2:])):
+        if size != 1 and stride != inner:
+            raise ValueError(f"{name} must have each token's elements contiguous")
+        inner *= size
+
+
+def _head_args(x, delta, A_log, B, C, D, delta_bias, initial_state):
+    if not isinstance(x, torch.Tensor) or x.dim() != 4 or not isinstance(B, torch.Tensor) or B.dim() != 4:
+        raise ValueError("x must be (b, L, H, P) and B (b, L, G, N)")
+    b, L, H, P = x.shape
+    G, N = B.shape[2:]
+    if G == 0 or H % G != 0:
+        raise ValueError(f"{H} heads do not divide into {G} groups")
+    dev = x.device
+    _check_tokens(x, "x", (b, L, H, P), x.dtype, dev)
+    _check_tokens(delta, "delta", (b, L, H), x.dtype, dev)
+    _check(A_log, "A_log", (H,), torch.float32, dev)
+    _check_tokens(B, "B", (b, L, G, N), x.dtype, dev)
+    _check_tokens(C, "C", (b, L, G, N), x.dtype, dev)
+    _check(D, "D", (H,), torch.float32, dev)
+    _check(delta_bias, "delta_bias", (H,), torch.float32, dev)
+    _check(initial_state, "initial_state", (b, H, P, N), torch.float32, dev)
+    strides = (ctypes.c_int64 * 8)(*(s for t in (x, delta, B, C) for s in t.stride()[:2]))
+    return b, L, H, P, N, G, dev, _dtype_code(x.dtype), strides
+
+
+def _bytes(t):
+    return 0 if t is None else t.numel() * t.element_size()
+
+
+def head_scan_fwd(x, delta, A_log, B, C, D, delta_bias=None, delta_softplus=True, initial_state=None,
+                  return_last_state=False, out=None, last_state=None, workspace=None):
+    """Head-wise selective scan on the GPU; returns y (and last_state if asked).
+
+    ``initial_state`` may be the ``last_state`` buffer itself (carried over in place).
+    """
+    b, L, H, P, N, G, dev, code, strides = _head_args(x, delta, A_log, B, C, D, delta_bias, initial_state)
+    y = torch.empty((b, L, H, P), dtype=x.dtype, device=dev) if out is None else out
+    _check(y, "out", (b, L, H, P), x.dtype, dev)
+    if return_last_state and last_state is None:
+        last_state = torch.empty((b, H, P, N), dtype=torch.float32, device=dev)
+    _check(last_state, "last_state", (b, H, P, N), torch.float32, dev)
+    if 0 in (b, L, H, P, N):
+        # No steps leave the initial state as it is; no state leaves the skip.
+        if last_state is not None:
+            if initial_state is None:
+                last_state.zero_()
+            elif initial_state.data_ptr() != last_state.data_ptr():
+                last_state.copy_(initial_state)
+        if y.numel():
+            y.copy_(x * D[:, None])
+        return (y, last_state) if return_last_state else y
+    if workspace is None:
+        workspace = _workspace(dev, int(lib.ss_head_scan_fwd_workspace_bytes(b, L, H, P, N, G, code)))
+    with torch.cuda.device(dev):
+        rc = lib.ss_head_scan_fwd(_ptr(x), _ptr(delta), _ptr(A_log), _ptr(B), _ptr(C), _ptr(D), _ptr(delta_bias),
+                                  int(bool(delta_softplus)), _ptr(initial_state), _ptr(y), _ptr(last_state),
+                                  b, L, H, P, N, G, code, strides, _ptr(workspace), _bytes(workspace), _stream(dev))
+    if rc != 0:
+        raise SSError(rc, "ss_head_scan_fwd")
+    return (y, last_state) if return_last_state else y
+
+
+def head_scan_bwd(x, delta, A_log, B, C, D, dy, delta_bias=None, delta_softplus=True, initial_state=None,
+                  dlast_state=None, workspace=None):
+    """Gradients of head_scan_fwd given dy (and dlast_state); returns a dict with dx, ddelta, dA_log, dB, dC, dD and,
+    where the input is given, ddelta_bias and dinitial_state."""
+    b, L, H, P, N, G, dev, code, strides = _head_args(x, delta, A_log, B, C, D, delta_bias, initial_state)
+    _check(dy, "dy", (b, L, H, P), x.dtype, dev)
+    _check(dlast_state, "dlast_state", (b, H, P, N), torch.float32, dev)
+    f32 = dict(dtype=torch.float32, device=dev)
+    own = dict(dtype=x.dtype, device=dev)
+    g = dict(dx=torch.empty((b, L, H, P), **own), ddelta=torch.empty((b, L, H), **own),
+             dA_log=torch.empty(H, **f32), dB=torch.empty((b, L, G, N), **own), dC=torch.empty((b, L, G, N), **own),
+             dD=torch.empty(H, **f32))
+    if delta_bias is not None:
+        g["ddelta_bias"] = torch.empty(H, **f32)
+    if initial_state is not None:
+        g["dinitial_state"] = torch.empty((b, H, P, N), **f32)
+    if 0 in (b, L, H, P, N):
+        for v in g.values():
+            v.zero_()
+        if initial_state is not None and dlast_state is not None:
+            g["dinitial_state"].copy_(dlast_state)
+        if g["dx"].numel():
+            g["dx"].copy_(dy * D[:, None])
+            g["dD"].copy_((dy.float() * x.float()).sum((0, 1, 3)))
+        return g
+    if workspace is None:
+        # Several times the size of the inputs: a buffer of its own, not kept.
+        workspace = torch.empty(int(lib.ss_head_scan_bwd_workspace_bytes(b, L, H, P, N, G, code)), dtype=torch.uint8,
+                                device=dev)
+    with torch.cuda.device(dev):
+        rc = lib.ss_head_scan_bwd(_ptr(x), _ptr(delta), _ptr(A_log), _ptr(B), _ptr(C), _ptr(D), _ptr(delta_bias),
+                                  int(bool(delta_softplus)), _ptr(initial_state), _ptr(dy), _ptr(dlast_state),
+                                  _ptr(g["dx"]), _ptr(g["ddelta"]), _ptr(g["dA_log"]), _ptr(g["dB"]), _ptr(g["dC"]),
+                                  _ptr(g["dD"]), _ptr(g.get("ddelta_bias")), _ptr(g.get("dinitial_state")),
+                                  b, L, H, P, N, G, code, strides, _ptr(workspace), _bytes(workspace), _stream(dev))
+    if rc != 0:
+        raise SSError(rc, "ss_head_scan_bwd")
+    return g
+
+
+class _HeadScan(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, delta, A_log, B, C, D, delta_bias, delta_softplus, initial_state):
+        ctx.delta_softplus = delta_softplus
+        ctx.save_for_backward(x, delta, A_log, B, C, D, delta_bias, initial_state)
+        return head_scan_fwd(x, delta, A_log, B, C, D, delta_bias, delta_softplus, initial_state,
+                             return_last_state=True)
+
+    @staticmethod
+    def backward(ctx, dy, dlast):
+        x, delta, A_log, B, C, D, delta_bias, initial_state = ctx.saved_tensors
+        g = head_scan_bwd(x, delta, A_log, B, C, D, dy.contiguous(), delta_bias, ctx.delta_softplus, initial_state,
+                          dlast.contiguous())
+        return (g["dx"], g["ddelta"], g["dA_log"], g["dB"], g["dC"], g["dD"], g.get("ddelta_bias"), None,
+                g.get("dinitial_state"))
+
+
+def head_scan(x, delta, A_log, B, C, D, delta_bias=None, delta_softplus=True, initial_state=None,
+              return_last_state=False):
+    """y of the head-wise scan (and last_state if asked), differentiable with respect to every tensor argument."""
+    y, last = _HeadScan.apply(x, delta, A_log, B, C, D, delta_bias, delta_softplus, initial_state)
+    return (y, last) if return_last_state else y
+
+
+def head_state_update(state, x, dt, A_log, B, C, D, dt_bias=None, dt_softplus=True, out=None):
+    """One decode step of the head-wise scan; ``state`` (b, H, P, N) fp32 is updated in place.  Returns y (b, H, P)."""
+    if state.dim() != 4 or B.dim() != 3:
+        raise ValueError("state must be (b, H, P, N) and B (b, G, N)")
+    b, H, P, N = state.shape
+    G = B.shape[1]
+    if G == 0 or H % G != 0:
+        raise ValueError(f"{H} heads do not divide into {G} groups")
+    dev = x.device
+    code = _dtype_code(x.dtype)
+    _check(state, "state", (b, H, P, N), torch.float32, dev)
+    _check(x, "x", (b, H, P), x.dtype, dev)
+    _check(dt, "dt", (b, H), x.dtype, dev)
+    _check(A_log, "A_log", (H,), torch.float32, dev)
+    _check(B, "B", (b, G, N), x.dtype, dev)
+    _check(C, "C", (b, G, N), x.dtype, dev)
+    _check(D, "D", (H,), torch.float32, dev)
+    _check(dt_bias, "dt_bias", (H,), torch.float32, dev)
+    y = torch.empty_like(x) if out is None else out
+    _check(y, "out", (b, H, P), x.dtype, dev)
+    if 0 in (b, H, P, N):
+        if y.numel():
+            y.copy_(x * D[:, None])
+        return y
+    with torch.cuda.device(dev):
+        rc = lib.ss_head_state_update(_ptr(state), _ptr(x), _ptr(dt), _ptr(A_log), _ptr(B), _ptr(C), _ptr(D),
+                                      _ptr(dt_bias), int(bool(dt_softplus)), _ptr(y), b, H, P, N, G, code,
+                                      _stream(dev))
+    if rc != 0:
+        raise SSError(rc, "ss_head_state_update")
+    return y
+
+
+def _rows(t, name, shape, dtype, device):
+    """Rows and row stride of a tensor whose rows (last dimension) are contiguous and evenly spaced."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    d = t.shape[-1]
+    if d > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    stride, span = None, 1
+    for size, st in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+        if size == 1:
+            continue
+        if stride is None:
+            stride = st
+        elif st != stride * span:
+            raise ValueError(f"{name} must have evenly spaced rows")
+        span *= size
+    stride = d if stride is None else stride
+    if stride < d and span > 1:
+        raise ValueError(f"{name} has rows that overlap")
+    return stride
+
+
+def _norm_shape(t, name):
+    if not isinstance(t, torch.Tensor) or t.dim() < 1:
+        raise ValueError(f"{name} must have a last dimension to take the norm over")
+    d = t.shape[-1]
+    return (t.numel() // d if d else 0), d
+
+
+def residual_norm_fwd(x, weight, residual=None, scale=None, eps=1e-5, residual_dtype=None, out=None,
+                      residual_out=None):
+    """r = residual + scale * x and out = r / rms(r) * weight; returns (out, r).
+
+    ``residual`` (and so r) is of x's type or fp32; without one, r has ``residual_dtype`` (x's type if not given).
+    ``residual_out`` may be the ``residual`` buffer itself.
+    """
+    rows, d = _norm_shape(x, "x")
+    dev = x.device
+    code = _dtype_code(x.dtype)
+    rt = residual.dtype if residual is not None else residual_out.dtype if residual_out is not None else \
+        residual_dtype or x.dtype
+    if rt not in (x.dtype, torch.float32):
+        raise TypeError(f"the residual must be {x.dtype} or float32, got {rt}")
+    x_stride = _rows(x, "x", x.shape, x.dtype, dev)
+    _check(weight, "weight", (d,), torch.float32, dev)
+    _check(residual, "residual", x.shape, rt, dev)
+    _check(scale, "scale", (d,), torch.float32, dev)
+    out = torch.empty(x.shape, dtype=x.dtype, device=dev) if out is None else out
+    residual_out = torch.empty(x.shape, dtype=rt, device=dev) if residual_out is None else residual_out
+    _check(out, "out", x.shape, x.dtype, dev)
+    _check(residual_out, "residual_out", x.shape, rt, dev)
+    if rows == 0 or d == 0:
+        return out, residual_out
+    with torch.cuda.device(dev):
+        rc = lib.ss_residual_norm_fwd(_ptr(x), _ptr(residual), _ptr(scale), _ptr(weight), _ptr(out),
+                                      _ptr(residual_out), rows, d, float(eps), code, _dtype_code(rt), x_stride,
+                                      _stream(dev))
+    if rc != 0:
+        raise SSError(rc, "ss_residual_norm_fwd")
+    return out, residual_out
+
+
+def residual_norm_bwd(dout, residual_out, weight, dresidual_out=None, x=None, scale=None, eps=1e-5, workspace=None,
+                      need_dresidual=True):
+    """Gradients of residual_norm_fwd from the gradients of both its outputs (``dresidual_out`` None: zero); returns a
+    dict with dx, dresidual, dweight and, with ``scale`` (which needs x), dscale.  Where x and the residual share a type
+    and there is no scale, dx and dresidual are one tensor."""
+    rows, d = _norm_shape(dout, "dout")
+    dev = dout.device
+    code = _dtype_code(dout.dtype)
+    rt = residual_out.dtype
+    if rt not in (dout.dtype, torch.float32):
+        raise TypeError(f"the residual must be {dout.dtype} or float32, got {rt}")
+    _check(dout, "dout", dout.shape, dout.dtype, dev)
+    _check(residual_out, "residual_out", dout.shape, rt, dev)
+    _check(dresidual_out, "dresidual_out", dout.shape, rt, dev)
+    _check(weight, "weight", (d,), torch.float32, dev)
+    _check(scale, "scale", (d,), torch.float32, dev)
+    x_stride = d
+    if scale is not None:
+        if x is None:
+            raise ValueError("the gradient of scale needs x")
+        x_stride = _rows(x, "x", dout.shape, dout.dtype, dev)
+    g = dict(dx=torch.empty_like(dout), dweight=torch.empty(d, dtype=torch.float32, device=dev))
+    apart = need_dresidual and (scale is not None or rt != dout.dtype)
+    if apart:
+        g["dresidual"] = torch.empty(dout.shape, dtype=rt, device=dev)
+    if scale is not None:
+        g["dscale"] = torch.empty(d, dtype=torch.float32, device=dev)
+    if rows == 0 or d == 0:
+        for v in g.values():
+            v.zero_()
+    else:
+        if workspace is None:
+            workspace = _workspace(dev, int(lib.ss_residual_norm_bwd_workspace_bytes(rows, d)))
+        with torch.cuda.device(dev):
+            rc = lib.ss_residual_norm_bwd(_ptr(dout), _ptr(dresidual_out), _ptr(residual_out),
+                                          _ptr(x) if scale is not None else None, _ptr(scale), _ptr(weight),
+                                          _ptr(g["dx"]), _ptr(g.get("dresidual")), _ptr(g["dweight"]),
+                                          _ptr(g.get("dscale")), rows, d, float(eps), code, _dtype_code(rt), x_stride,
+                                          _ptr(workspace), _bytes(workspace), _stream(dev))
+        if rc != 0:
+            raise SSError(rc, "ss_residual_norm_bwd")
+    if need_dresidual and not apart:
+        g["dresidual"] = g["dx"]
+    return g
+
+
+class _ResidualNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, residual, scale, eps, residual_dtype):
+        out, r = residual_norm_fwd(x, weight, residual, scale, eps, residual_dtype)
+        ctx.eps = eps
+        ctx.has_residual = residual is not None
+        ctx.save_for_backward(x if scale is not None else None, weight, scale, r)
+        return out, r
+
+    @staticmethod
+    def backward(ctx, dout, dr):
+        x, weight, scale, r = ctx.saved_tensors
+        g = residual_norm_bwd(dout.contiguous(), r, weight, dr.contiguous(), x, scale, ctx.eps,
+                              need_dresidual=ctx.has_residual)
+        return g["dx"], g["dweight"], g.get("dresidual"), g.get("dscale"), None, None
+
+
+def residual_norm(x, weight, residual=None, scale=None, eps=1e-5, residual_dtype=None):
+    """(out, r) of residual_norm_fwd, differentiable with respect to every tensor argument."""
+    return _ResidualNorm.apply(x, weight, residual, scale, eps, residual_dtype)
+
+
+def gated_norm_fwd(y, z, weight, groups=1, eps=1e-5, norm_before_gate=False, out=None):
+    """v / rms(v) * weight per group of channels with v = y * silu(z), or with ``norm_before_gate`` v = y and the
+    result times silu(z)."""
+    rows, d = _norm_shape(y, "y")
+    dev = y.device
+    code = _dtype_code(y.dtype)
+    y_stride = _rows(y, "y", y.shape, y.dtype, dev)
+    z_stride = _rows(z, "z", y.shape, y.dtype, dev)
+    _check(weight, "weight", (d,), torch.float32, dev)
+    out = torch.empty(y.shape, dtype=y.dtype, device=dev) if out is None else out
+    _check(out, "out", y.shape, y.dtype, dev)
+    if rows == 0 or d == 0:
+        return out
+    with torch.cuda.device(dev):
+        rc = lib.ss_gated_norm_fwd(_ptr(y), _ptr(z), _ptr(weight), _ptr(out), rows, d, int(groups), float(eps),
+                                   int(bool(norm_before_gate)), code, y_stride, z_stride, _stream(dev))
+    if rc != 0:
+        raise SSError(rc, "ss_gated_norm_fwd")
+    return out
+
+
+def gated_norm_bwd(dout, y, z, weight, groups=1, eps=1e-5, norm_before_gate=False, workspace=None):
+    """Gradients of gated_norm_fwd; returns a dict with dy, dz and dweight."""
+    rows, d = _norm_shape(y, "y")
+    dev = y.device
+    code = _dtype_code(y.dtype)
+    y_stride = _rows(y, "y", y.shape, y.dtype, dev)
+    z_stride = _rows(z, "z", y.shape, y.dtype, dev)
+    _check(dout, "dout", y.shape, y.dtype, dev)
+    _check(weight, "weight", (d,), torch.float32, dev)
+    g = dict(dy=torch.empty(y.shape, dtype=y.dtype, device=dev), dz=torch.empty(y.shape, dtype=y.dtype, device=dev),
+             dweight=torch.empty(d, dtype=torch.float32, device=dev))
+    if rows == 0 or d == 0:
+        for v in g.values():
+            v.zero_()
+        return g
+    if workspace is None:
+        workspace = _workspace(dev, int(lib.ss_gated_norm_bwd_workspace_bytes(rows, d, int(groups))))
+    with torch.cuda.device(dev):
+        rc = lib.ss_gated_norm_bwd(_ptr(dout), _ptr(y), _ptr(z), _ptr(weight), _ptr(g["dy"]), _ptr(g["dz"]),
+                                   _ptr(g["dweight"]), rows, d, int(groups), float(eps), int(bool(norm_before_gate)),
+                                   code, y_stride, z_stride, _ptr(workspace), _bytes(workspace), _stream(dev))
+    if rc != 0:
+        raise SSError(rc, "ss_gated_norm_bwd")
+    return g
+
+
+class _GatedNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, y, z, weight, groups, eps, norm_before_gate):
+        ctx.save_for_backward(y, z, weight)
+        ctx.args = (groups, eps, norm_before_gate)
+        return gated_norm_fwd(y, z, weight, groups, eps, norm_before_gate)
+
+    @staticmethod
+    def backward(ctx, dout):
+        y, z, weight = ctx.saved_tensors
+        g = gated_norm_bwd(dout.contiguous(), y, z, weight, *ctx.args)
+        return g["dy"], g["dz"], g["dweight"], None, None, None
+
+
+def gated_norm(y, z, weight, groups=1, eps=1e-5, norm_before_gate=False):
+    """gated_norm_fwd, differentiable with respect to y, z and weight."""
+    return _GatedNorm.apply(y, z, weight, groups, eps, norm_before_gate)

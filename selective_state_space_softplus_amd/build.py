@@ -23,11 +23,12 @@ LIBRARY = os.path.join(PKG, "libss_scan.so")
 # The VALU issue-rate probe that bench.py --valu-probe runs (a measurement aid).
 PROBE_SOURCE = os.path.join(CSRC, "valu_probe.hip")
 PROBE_LIBRARY = os.path.join(PKG, "libss_probe.so")
-# The C ABI and the small kernels in one translation unit; the scan_seq and
+# The scans' C ABI and small kernels in one translation unit, the operators
+# around the head-wise scan in two; the scan_seq and
 # scan_bwd launchers (launch_seq.h, launch_bwd.h) are instantiated once per
 # input type and launch shape, each in a small generated unit of its own, so
 # that the kernels compile in parallel.
-SOURCES = [os.path.join(CSRC, "ss_scan.hip")]
+SOURCES = [os.path.join(CSRC, "ss_scan.hip"), os.path.join(CSRC, "head_scan.hip"), os.path.join(CSRC, "norms.hip")]
 INPUT_TYPES = ("uint16_t", "float")
 SEQ_SHAPES = ((1, 2), (4, 2), (4, 4), (8, 2), (8, 4), (8, 8))   # must cover ss_host::seq_shape
 BWD_SHAPES = ((1, 2, False), (4, 2, False), (8, 2, False), (8, 2, True))   # must cover ss_host::bwd_shape

@@ -1,0 +1,222 @@
+// block_device.h -- device helpers of the block's operators (gfx950): operand
+// fragments of the matrix instructions, LDS tiles, and reductions.
+#pragma once
+
+#include "ss_device.h"
+
+namespace ss {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+// 16 bytes of global memory at any element's address: global accesses need no
+// more than their element's alignment here, so rows of odd length or offset
+// take the same vector accesses as aligned ones.
+typedef u32x4 u32x4_at2 __attribute__((aligned(2)));
+typedef u32x4 u32x4_at4 __attribute__((aligned(4)));
+__device__ __forceinline__ u32x4 load16(const uint16_t* p) { return *reinterpret_cast<const u32x4_at2*>(p); }
+__device__ __forceinline__ u32x4 load16(const float* p) { return *reinterpret_cast<const u32x4_at4*>(p); }
+__device__ __forceinline__ void store16(uint16_t* p, u32x4 v) { *reinterpret_cast<u32x4_at2*>(p) = v; }
+__device__ __forceinline__ void store16(float* p, u32x4 v) { *reinterpret_cast<u32x4_at4*>(p) = v; }
+
+// Operands of a 16 x 16 product over 32 values of k.  A lane l holds 8 values
+// of k, those of lane group l / 16, for row (first operand) or column (second
+// operand) l % 16; the product's lane l holds rows 4 (l / 16) + 0..3 of column
+// l % 16.  Which 8 of the 32 k a lane group holds is free as long as both
+// operands agree.
+//   bf16: one 16x16x32 matrix instruction.
+//   fp32: eight 16x16x4 ones (k one per lane group and instruction), exact to
+//         fp32; the chip has no faster form that is.
+template <typename T> struct Mat;
+
+template <> struct Mat<uint16_t> {
+    using Frag = bf16x8;
+    static constexpr int kWide = 3;
+    // 8 consecutive elements at p (16-byte aligned).
+    static __device__ __forceinline__ Frag load(const uint16_t* p) {
+        return __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4*>(p));
+    }
+    // 4 consecutive elements at p and 4 at q (8-byte aligned).
+    static __device__ __forceinline__ Frag load_2x4(const uint16_t* p, const uint16_t* q) {
+        const u32x2 a = *reinterpret_cast<const u32x2*>(p), b = *reinterpret_cast<const u32x2*>(q);
+        return __builtin_bit_cast(bf16x8, u32x4{a.x, a.y, b.x, b.y});
+    }
+    // 8 elements `stride` apart.
+    static __device__ __forceinline__ Frag gather(const uint16_t* p, int stride) {
+        u32x4 v;
+#pragma unroll
+        for (int i = 0; i < 4; i++) v[i] = uint32_t(p[2 * i * stride]) | uint32_t(p[(2 * i + 1) * stride]) << 16;
+        return __builtin_bit_cast(bf16x8, v);
+    }
+    // Rounded to nearest even: the operand's only rounding.
+    static __device__ __forceinline__ Frag pack(f32x8 v) {
+        return __builtin_bit_cast(bf16x8, u32x4{f32x2_to_bf16x2(v[0], v[1]), f32x2_to_bf16x2(v[2], v[3]),
+                                               f32x2_to_bf16x2(v[4], v[5]), f32x2_to_bf16x2(v[6], v[7])});
+    }
+    static __device__ __forceinline__ f32x8 unpack(Frag f) {
+        const u32x4 v = __builtin_bit_cast(u32x4, f);
+        f32x8 o;
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            o[2 * i] = __uint_as_float(v[i] << 16);
+            o[2 * i + 1] = __uint_as_float(v[i] & 0xffff0000u);
+        }
+        return o;
+    }
+    // An fp32 operand as three bf16 ones whose sum it is: 8 + 8 + 8 bits of
+    // its 24 (each remainder is exact), so products with an exact bf16 operand
+    // sum to what fp32 multiplication would.
+    static __device__ __forceinline__ void split(f32x8 v, Frag (&f)[3]) {
+#pragma unroll
+        for (int i = 0; i < 3; i++) {
+            f[i] = pack(v);
+            if (i < 2) v -= unpack(f[i]);
+        }
+    }
+    static __device__ __forceinline__ f32x4 mma(Frag a, Frag b, f32x4 c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+    }
+};
+
+template <> struct Mat<float> {
+    using Frag = f32x8;
+    static constexpr int kWide = 1;
+    static __device__ __forceinline__ Frag load(const float* p) {
+        const f32x4 a = *reinterpret_cast<const f32x4*>(p), b = *reinterpret_cast<const f32x4*>(p + 4);
+        return Frag{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+    }
+    static __device__ __forceinline__ Frag load_2x4(const float* p, const float* q) {
+        const f32x4 a = *reinterpret_cast<const f32x4*>(p), b = *reinterpret_cast<const f32x4*>(q);
+        return Frag{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+    }
+    static __device__ __forceinline__ Frag gather(const float* p, int stride) {
+        Frag v;
+#pragma unroll
+        for (int i = 0; i < 8; i++) v[i] = p[i * stride];
+        return v;
+    }
+    static __device__ __forceinline__ Frag pack(f32x8 v) { return v; }
+    static __device__ __forceinline__ f32x8 unpack(Frag f) { return f; }
+    static __device__ __forceinline__ void split(f32x8 v, Frag (&f)[1]) { f[0] = v; }
+    static __device__ __forceinline__ f32x4 mma(Frag a, Frag b, f32x4 c) {
+#pragma unroll
+        for (int i = 0; i < 8; i++) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[i], b[i], c, 0, 0, 0);
+        return c;
+    }
+};
+
+// a * (f[0] + f[1] + ...), the small parts first.
+template <typename T>
+__device__ __forceinline__ f32x4 mma_wide(typename Mat<T>::Frag a, const typename Mat<T>::Frag (&f)[Mat<T>::kWide],
+                                          f32x4 c) {
+#pragma unroll
+    for (int i = Mat<T>::kWide - 1; i >= 0; i--) c = Mat<T>::mma(a, f[i], c);
+    return c;
+}
+
+// 4 values as 4 consecutive LDS elements (8- or 16-byte aligned).
+__device__ __forceinline__ void store4(uint16_t* p, f32x4 v) {
+    *reinterpret_cast<u32x2*>(p) = u32x2{f32x2_to_bf16x2(v[0], v[1]), f32x2_to_bf16x2(v[2], v[3])};
+}
+__device__ __forceinline__ void store4(float* p, f32x4 v) { *reinterpret_cast<f32x4*>(p) = v; }
+
+template <typename T>
+__device__ __forceinline__ float widen(T v) {
+    if constexpr (sizeof(T) == 2) return bf16_to_f32(v);
+    else return v;
+}
+template <typename T>
+__device__ __forceinline__ T narrow(float v) {
+    if constexpr (sizeof(T) == 2) return f32_to_bf16(v);
+    else return v;
+}
+
+// Whether any element of a 16-byte vector is infinite or NaN (its exponent
+// bits all ones): adding one at the exponent's end then carries into the sign
+// bit, which was cleared.
+template <typename T>
+__device__ __forceinline__ bool any_non_finite(u32x4 v) {
+    constexpr uint32_t mask = sizeof(T) == 2 ? 0x7f807f80u : 0x7f800000u;
+    constexpr uint32_t one = sizeof(T) == 2 ? 0x00800080u : 0x00800000u;
+    constexpr uint32_t top = sizeof(T) == 2 ? 0x80008000u : 0x80000000u;
+    uint32_t r = 0;
+#pragma unroll
+    for (int i = 0; i < 4; i++) r |= (v[i] & mask) + one;
+    return (r & top) != 0;
+}
+
+// A 64 x COLS tile of a strided source on its way to LDS: 256 threads hold
+// 16-byte vectors.  Rows at and beyond `rows` and columns at and beyond `cols`
+// are zero.  In LDS a row takes kLd elements, 16 bytes more than its data, so
+// that 16 rows' accesses at one column spread over the banks.
+template <typename T, int COLS>
+struct Tile {
+    static constexpr int kVec = 16 / int(sizeof(T));
+    static constexpr int kLd = COLS + kVec;
+    static constexpr int kPerRow = COLS / kVec;
+    static constexpr int kN = 64 * kPerRow / 256;
+    static constexpr int kElems = 64 * kLd;
+    static_assert(64 * kPerRow % 256 == 0, "whole vectors per thread");
+    u32x4 v[kN];
+
+    __device__ __forceinline__ void load(const T* src, int64_t stride, int rows, int cols) {
+#pragma unroll
+        for (int i = 0; i < kN; i++) {
+            const int at = int(threadIdx.x) + 256 * i, row = at / kPerRow, col = at % kPerRow * kVec;
+            u32x4 w = {0, 0, 0, 0};
+            if (row < rows && col < cols) {
+                const T* p = src + row * stride + col;
+                if (col + kVec <= cols) {
+                    w = load16(p);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < kVec; e++)
+                        if (col + e < cols) {
+                            if constexpr (sizeof(T) == 2) w[e / 2] |= uint32_t(p[e]) << (16 * (e % 2));
+                            else w[e] = __float_as_uint(p[e]);
+                        }
+                }
+            }
+            v[i] = w;
+        }
+    }
+    __device__ __forceinline__ void store(T* lds) const {
+#pragma unroll
+        for (int i = 0; i < kN; i++) {
+            const int at = int(threadIdx.x) + 256 * i, row = at / kPerRow, col = at % kPerRow * kVec;
+            *reinterpret_cast<u32x4*>(lds + row * kLd + col) = v[i];
+        }
+    }
+    __device__ __forceinline__ bool non_finite() const {
+        bool r = false;
+#pragma unroll
+        for (int i = 0; i < kN; i++) r |= any_non_finite<T>(v[i]);
+        return r;
+    }
+};
+
+// Sum over the 16 lanes of a lane group, over the 4 groups, over the wave; in
+// every lane, in an order that does not vary.
+__device__ __forceinline__ float sum_lanes16(float v) {
+#pragma unroll
+    for (int m = 1; m < 16; m <<= 1) v += __shfl_xor(v, m);
+    return v;
+}
+__device__ __forceinline__ float sum_groups4(float v) {
+    v += __shfl_xor(v, 16);
+    return v + __shfl_xor(v, 32);
+}
+__device__ __forceinline__ float sum_wave(float v) { return sum_groups4(sum_lanes16(v)); }
+
+// Workgroups are handed to the 8 XCDs in turn.  With `total` of them, the
+// workgroup `id` takes piece piece_of(id, total): each XCD then holds one
+// contiguous range of pieces, and pieces that share inputs share an L2.
+__device__ __forceinline__ uint32_t piece_of(uint32_t id, uint32_t total) {
+    const uint32_t per = total / 8, rem = total % 8, xcd = id % 8, slot = id / 8;
+    return xcd * per + umin(xcd, rem) + slot;
+}
+
+}  // namespace ss

@@ -1,0 +1,839 @@
+// head_kernels.h -- the head-wise selective scan on matrix cores (gfx950).
+//
+// One decay per head and step and a (P, N) state per head:
+//     S_t = a_t S_{t-1} + s_t x_t B_t^T,   y_t = S_t C_t + D x_t,
+// s_t the step size and a_t = exp(s_t A).  Steps are taken in chunks of 64.
+// With c_i the running sum of log a inside a chunk, L_ij = exp(c_i - c_j) for
+// j <= i and 0 else, S the state before the chunk:
+//     y_i = sum_j L_ij (C_i . B_j) s_j x_j + exp(c_i) S C_i + D x_i
+//     S'  = exp(c_63) S + sum_j exp(c_63 - c_j) s_j x_j B_j^T
+// which are products of 64 x 64, 64 x N and 64 x P tiles.  The exponents are
+// never positive for s >= 0, so nothing overflows.  c is summed in 64 bits and
+// kept as two floats: with one, a step that decays much would cost the later
+// differences their digits (measured: 1.1e-5 relative after a decay of 2^-200,
+// 1e-6 with two).
+//
+// A workgroup of 4 waves holds the state of one head and a slab of 64 of its P
+// channels in accumulators, wave w channels 16 w .. 16 w + 15, and walks over
+// the chunks of its segment of the sequence.
+#pragma once
+
+#include "block_device.h"
+
+namespace ss {
+
+constexpr int kHeadChunk = 64;
+constexpr int kHeadSlab = 64;
+
+struct HeadParams {
+    const void *x, *delta, *B, *C, *dy;
+    const float *A_log, *D, *bias, *h0, *dlast;
+    void *y, *dx, *ddelta, *dB, *dC;
+    float *last, *dA_log, *dD, *dbias, *dh0;
+    int64_t xb, xt, deltab, deltat, Bb, Bt, Cb, Ct;   // batch and time strides, elements
+    int64_t b, L;
+    int H, P, N, G;
+    int slabs, chunks;      // ceil(P / 64), ceil(L / 64)
+    int nseg, seg_chunks;   // segments of the sequence, chunks in each but the last
+    int softplus;
+    float *seg_state;       // (b, H, slabs, nseg, NP, 64): the segments' states
+    float *seg_decay;       // (b, H, nseg): log2 of the segments' decays
+    float *chunk_s;         // (b, H, slabs, chunks, NP, 64): the state before every chunk
+    float *chunk_q;         //                               the adjoint state after every chunk
+    float *partial;         // (3, b * chunks, H): a chunk's share of dA_log, dbias, dD
+    float *dbc;             // (2, blocks, b, L, G, N): shares of dB and dC by head block
+    int blocks, per_block;  // head blocks of a group and heads in each
+};
+
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+
+// Decays of a chunk: lane t of a wave takes step t.
+struct Gate {
+    float step, raw;   // step size and its argument
+    f32x2 c;           // running sum of log2 a, as a sum of two floats
+};
+
+// a - b of two such sums, rounded to the difference's own digits.
+__device__ __forceinline__ float c_diff(f32x2 a, f32x2 b) { return (a.x - b.x) + (a.y - b.y); }
+
+// The least log2 of one step's decay: 2^-200 is 0 in fp32, and a finite sum has differences.
+constexpr float kLeastDecay = -200.0f;
+
+template <typename T>
+__device__ __forceinline__ float gate_load(const HeadParams& p, int64_t bi, int h, int chunk) {
+    const int64_t t = int64_t(chunk) * kHeadChunk + (threadIdx.x & 63);
+    if (t >= p.L) return 0.0f;
+    return Elem<T>::load(static_cast<const T*>(p.delta), bi * p.deltab + t * p.deltat + h);
+}
+
+__device__ __forceinline__ Gate make_gate(float delta, float bias, float a2, int use_softplus, bool valid) {
+    Gate g;
+    g.raw = delta + bias;
+    g.step = valid ? (use_softplus ? softplus(g.raw) : g.raw) : 0.0f;
+    double c = valid ? fmaxf(g.step * a2, kLeastDecay) : 0.0f;
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1) {
+        const double up = __shfl_up(c, m);
+        c += lane >= m ? up : 0.0;
+    }
+    g.c.x = float(c);
+    g.c.y = float(c - double(g.c.x));
+    return g;
+}
+
+// Rows of the chunk that are inside the sequence.
+__device__ __forceinline__ int chunk_rows(const HeadParams& p, int chunk) {
+    return int(imin(kHeadChunk, p.L - int64_t(chunk) * kHeadChunk));
+}
+
+enum class StateMode { Local, Chunks };
+
+// States over the sequence.
+//   REV false: S over chunks in order, from x and B weighted by exp(c_63 - c_j) s_j.
+//   REV true:  the adjoint state Q backwards, Q = exp(c_63) Q' + sum_i exp(c_i) dy_i C_i^T.
+//   Local:  a segment's state from zero, to seg_state, and its decay to seg_decay.
+//   Chunks: from seg_state (several segments) or the given end state; the state
+//           at entry to every chunk goes to chunk_s or chunk_q, the last one to
+//           last / dh0 where a segment is the whole sequence.
+template <typename T, int NP, bool REV, StateMode MODE>
+__global__ __launch_bounds__(256) void head_states(HeadParams p) {
+    using M = Mat<T>;
+    using TileK = Tile<T, NP>;
+    using TileV = Tile<T, kHeadSlab>;
+    extern __shared__ __align__(16) float smem[];
+    T* const k_lds = reinterpret_cast<T*>(smem);
+    T* const v_lds = k_lds + TileK::kElems;
+    f32x2* const c_lds = reinterpret_cast<f32x2*>(v_lds + TileV::kElems);   // c of the chunk
+    float* const s_lds = reinterpret_cast<float*>(c_lds + 64);                                        // steps
+
+    const uint32_t piece = piece_of(blockIdx.x, gridDim.x);
+    const int hs = int(piece % uint32_t(p.H * p.slabs)), h = hs / p.slabs, slab = hs % p.slabs;
+    const uint32_t rest = piece / uint32_t(p.H * p.slabs);
+    const int seg = int(rest % uint32_t(p.nseg));
+    const int64_t bi = rest / uint32_t(p.nseg);
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, lr = lane & 15, lg = lane >> 4;
+    const int pc = 16 * wave + lr, pg = slab * kHeadSlab + pc;   // channel in the slab, in the head
+    const int64_t bh = bi * p.H + h;
+    const int g = h / (p.H / p.G);
+    const int first = seg * p.seg_chunks, last = int(imin(first + p.seg_chunks, p.chunks)) - 1;
+
+    const T* const kb = REV ? static_cast<const T*>(p.C) + bi * p.Cb + int64_t(g) * p.N
+                            : static_cast<const T*>(p.B) + bi * p.Bb + int64_t(g) * p.N;
+    const int64_t kt = REV ? p.Ct : p.Bt;
+    const T* const vb = (REV ? static_cast<const T*>(p.dy) + bi * p.L * p.H * p.P
+                             : static_cast<const T*>(p.x) + bi * p.xb) + int64_t(h) * p.P + slab * kHeadSlab;
+    const int64_t vt = REV ? int64_t(p.H) * p.P : p.xt;
+    const int vcols = p.P - slab * kHeadSlab;
+    const float a2 = a2_from_alog(p.A_log[h]), bias = p.bias ? p.bias[h] : 0.0f;
+
+    f32x4 acc[NP / 16];
+    float* const seg_at = p.seg_state + ((bh * p.slabs + slab) * p.nseg + seg) * (NP * 64);
+    const float* const init = REV ? p.dlast : p.h0;
+#pragma unroll
+    for (int nt = 0; nt < NP / 16; nt++)
+#pragma unroll
+        for (int r = 0; r < 4; r++) {
+            const int n = 16 * nt + 4 * lg + r;
+            float v = 0.0f;
+            if (MODE == StateMode::Chunks) {
+                if (p.nseg > 1) v = seg_at[n * 64 + pc];
+                else if (init && n < p.N && pg < p.P) v = init[(bh * p.P + pg) * p.N + n];
+            }
+            acc[nt][r] = v;
+        }
+
+    TileK tk;
+    TileV tv;
+    float dl;
+    auto fetch = [&](int ck) {
+        const int64_t t0 = int64_t(ck) * kHeadChunk;
+        const int rows = chunk_rows(p, ck);
+        tk.load(kb + t0 * kt, kt, rows, p.N);
+        tv.load(vb + t0 * vt, vt, rows, vcols);
+        dl = gate_load<T>(p, bi, h, ck);
+    };
+    const int count = last - first + 1;
+    fetch(REV ? last : first);
+    float total = 0.0f;
+    for (int it = 0; it < count; it++) {
+        const int ck = REV ? last - it : first + it;
+        __syncthreads();
+        tk.store(k_lds);
+        tv.store(v_lds);
+        if (wave == 0) {
+            const Gate gt = make_gate(dl, bias, a2, p.softplus, lane < chunk_rows(p, ck));
+            c_lds[lane] = gt.c;
+            s_lds[lane] = gt.step;
+        }
+        const bool odd = !REV && tv.non_finite();
+        const bool scalar = __syncthreads_or(odd) != 0;
+        if (it + 1 < count) fetch(REV ? ck - 1 : ck + 1);
+        if (MODE == StateMode::Chunks) {
+            float* const to = (REV ? p.chunk_q : p.chunk_s) + ((bh * p.slabs + slab) * p.chunks + ck) * (NP * 64);
+#pragma unroll
+            for (int nt = 0; nt < NP / 16; nt++)
+#pragma unroll
+                for (int r = 0; r < 4; r++) to[(16 * nt + 4 * lg + r) * 64 + pc] = acc[nt][r];
+        }
+        const f32x2 cq = c_lds[63];
+        const float decay = exp2_hw(cq.x);
+        total += cq.x;
+#pragma unroll
+        for (int nt = 0; nt < NP / 16; nt++) acc[nt] *= decay;
+        if (!scalar) {
+#pragma unroll
+            for (int kk = 0; kk < 2; kk++) {
+                const int j0 = 32 * kk + 8 * lg;
+                f32x8 wv = M::unpack(M::gather(v_lds + j0 * TileV::kLd + pc, TileV::kLd));
+#pragma unroll
+                for (int e = 0; e < 8; e++)
+                    wv[e] *= REV ? exp2_hw(c_lds[j0 + e].x) : exp2_hw(c_diff(cq, c_lds[j0 + e])) * s_lds[j0 + e];
+                typename M::Frag w[M::kWide];
+                M::split(wv, w);
+#pragma unroll
+                for (int nt = 0; nt < NP / 16; nt++)
+                    acc[nt] = mma_wide<T>(M::gather(k_lds + j0 * TileK::kLd + 16 * nt + lr, TileK::kLd), w, acc[nt]);
+            }
+        } else {
+            // An infinite or NaN x: multiply-adds give what the definition gives, where a sum of parts of it would not.
+            for (int j = 0; j < 64; j++) {
+                const float wx = exp2_hw(c_diff(cq, c_lds[j])) * s_lds[j] * widen(v_lds[j * TileV::kLd + pc]);
+#pragma unroll
+                for (int nt = 0; nt < NP / 16; nt++)
+#pragma unroll
+                    for (int r = 0; r < 4; r++)
+                        acc[nt][r] += wx * widen(k_lds[j * TileK::kLd + 16 * nt + 4 * lg + r]);
+            }
+        }
+    }
+    if (MODE == StateMode::Local) {
+#pragma unroll
+        for (int nt = 0; nt < NP / 16; nt++)
+#pragma unroll
+            for (int r = 0; r < 4; r++) seg_at[(16 * nt + 4 * lg + r) * 64 + pc] = acc[nt][r];
+        if (slab == 0 && threadIdx.x == 0) p.seg_decay[bh * p.nseg + seg] = total;
+    } else if (p.nseg == 1) {
+        float* const out = REV ? p.dh0 : p.last;
+        if (out && pg < p.P)
+#pragma unroll
+            for (int nt = 0; nt < NP / 16; nt++)
+#pragma unroll
+                for (int r = 0; r < 4; r++) {
+                    const int n = 16 * nt + 4 * lg + r;
+                    if (n < p.N) out[(bh * p.P + pg) * p.N + n] = acc[nt][r];
+                }
+    }
+}
+
+// The segments' states from zero, in place, become the states at the segments'
+// starts (REV: the adjoint states at their ends), walking from the given end
+// state; what is left past the last one goes to last / dh0.
+template <int NP, bool REV>
+__global__ __launch_bounds__(256) void head_carry(HeadParams p) {
+    const int64_t at = int64_t(blockIdx.x) * 256 + threadIdx.x;   // (b, h, slab, n, channel)
+    const int64_t total = p.b * p.H * p.slabs * (NP * 64);
+    if (at >= total) return;
+    const int pc = int(at & 63), n = int(at >> 6) & (NP - 1);
+    const int64_t bhs = at / (NP * 64), bh = bhs / p.slabs;
+    const int pg = int(bhs % p.slabs) * kHeadSlab + pc;
+    const bool inside = pg < p.P && n < p.N;
+    const float* const init = REV ? p.dlast : p.h0;
+    float s = init && inside ? init[(bh * p.P + pg) * p.N + n] : 0.0f;
+    float* const states = p.seg_state + bhs * p.nseg * (NP * 64) + (at & (NP * 64 - 1));
+    for (int i = 0; i < p.nseg; i++) {
+        const int seg = REV ? p.nseg - 1 - i : i;
+        float* const q = states + int64_t(seg) * (NP * 64);
+        const float local = *q;
+        *q = s;
+        s = exp2_hw(p.seg_decay[bh * p.nseg + seg]) * s + local;
+    }
+    float* const out = REV ? p.dh0 : p.last;
+    if (out && inside) out[(bh * p.P + pg) * p.N + n] = s;
+}
+
+// The outputs of a segment, and with one segment the last state.
+//
+// Per chunk: the scores B C^T, weighted, go through LDS as the first operand of
+// the product with x; the state, held as the accumulators of the update, is
+// rounded to bf16 in place as the second operand of the readout (its rows n
+// are the product's k: lane group g holds n = 4 g + 0..3 of two 16-row tiles).
+template <typename T, int NP>
+__global__ __launch_bounds__(256) void head_out(HeadParams p) {
+    using M = Mat<T>;
+    using TileK = Tile<T, NP>;
+    using TileV = Tile<T, kHeadSlab>;
+    extern __shared__ __align__(16) float smem[];
+    T* const b_lds = reinterpret_cast<T*>(smem);
+    T* const q_lds = b_lds + TileK::kElems;
+    T* const x_lds = q_lds + TileK::kElems;
+    T* const m_lds = x_lds + TileV::kElems;    // weighted scores [i][j]
+    f32x2* const c_lds = reinterpret_cast<f32x2*>(m_lds + TileV::kElems);
+    float* const s_lds = reinterpret_cast<float*>(c_lds + 64);
+
+    const uint32_t piece = piece_of(blockIdx.x, gridDim.x);
+    const int hs = int(piece % uint32_t(p.H * p.slabs)), h = hs / p.slabs, slab = hs % p.slabs;
+    const uint32_t rest = piece / uint32_t(p.H * p.slabs);
+    const int seg = int(rest % uint32_t(p.nseg));
+    const int64_t bi = rest / uint32_t(p.nseg);
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, lr = lane & 15, lg = lane >> 4;
+    const int pc = 16 * wave + lr, pg = slab * kHeadSlab + pc;
+    const int64_t bh = bi * p.H + h;
+    const int g = h / (p.H / p.G);
+    const int first = seg * p.seg_chunks, last = int(imin(first + p.seg_chunks, p.chunks)) - 1;
+
+    const T* const bb = static_cast<const T*>(p.B) + bi * p.Bb + int64_t(g) * p.N;
+    const T* const cb = static_cast<const T*>(p.C) + bi * p.Cb + int64_t(g) * p.N;
+    const T* const xb = static_cast<const T*>(p.x) + bi * p.xb + int64_t(h) * p.P + slab * kHeadSlab;
+    T* const yb = static_cast<T*>(p.y) + (bi * p.L * p.H + h) * p.P;
+    const int64_t yt = int64_t(p.H) * p.P;
+    const int vcols = p.P - slab * kHeadSlab;
+    const float a2 = a2_from_alog(p.A_log[h]), bias = p.bias ? p.bias[h] : 0.0f, skip = p.D[h];
+
+    f32x4 acc[NP / 16];
+    const float* const seg_at = p.seg_state + ((bh * p.slabs + slab) * p.nseg + seg) * (NP * 64);
+#pragma unroll
+    for (int nt = 0; nt < NP / 16; nt++)
+#pragma unroll
+        for (int r = 0; r < 4; r++) {
+            const int n = 16 * nt + 4 * lg + r;
+            float v = 0.0f;
+            if (p.nseg > 1) v = seg_at[n * 64 + pc];
+            else if (p.h0 && n < p.N && pg < p.P) v = p.h0[(bh * p.P + pg) * p.N + n];
+            acc[nt][r] = v;
+        }
+
+    TileK tb, tc;
+    TileV tx;
+    float dl;
+    auto fetch = [&](int ck) {
+        const int64_t t0 = int64_t(ck) * kHeadChunk;
+        const int rows = chunk_rows(p, ck);
+        tb.load(bb + t0 * p.Bt, p.Bt, rows, p.N);
+        tc.load(cb + t0 * p.Ct, p.Ct, rows, p.N);
+        tx.load(xb + t0 * p.xt, p.xt, rows, vcols);
+        dl = gate_load<T>(p, bi, h, ck);
+    };
+    fetch(first);
+    for (int ck = first; ck <= last; ck++) {
+        const int rows = chunk_rows(p, ck);
+        __syncthreads();
+        tb.store(b_lds);
+        tc.store(q_lds);
+        tx.store(x_lds);
+        if (wave == 0) {
+            const Gate gt = make_gate(dl, bias, a2, p.softplus, lane < rows);
+            c_lds[lane] = gt.c;
+            s_lds[lane] = gt.step;
+        }
+        const bool scalar = __syncthreads_or(tx.non_finite()) != 0;
+        if (ck < last) fetch(ck + 1);
+
+        // Scores of rows i = 16 wave + lr, columns j = 16 jt + 4 lg + r, j <= i.
+        {
+            const int i = 16 * wave + lr;
+            const f32x2 ci = c_lds[i];
+            for (int jt = 0; jt <= (wave | 1); jt++) {
+                f32x4 s = {0, 0, 0, 0};
+                if (jt <= wave) {
+#pragma unroll
+                    for (int kk = 0; kk < NP / 32; kk++)
+                        s = M::mma(M::load(b_lds + (16 * jt + lr) * TileK::kLd + 32 * kk + 8 * lg),
+                                   M::load(q_lds + i * TileK::kLd + 32 * kk + 8 * lg), s);
+#pragma unroll
+                    for (int r = 0; r < 4; r++) {
+                        const int j = 16 * jt + 4 * lg + r;
+                        s[r] = j <= i ? s[r] * (exp2_hw(c_diff(ci, c_lds[j])) * s_lds[j]) : 0.0f;
+                    }
+                }
+                store4(m_lds + i * TileV::kLd + 16 * jt + 4 * lg, s);
+            }
+        }
+        __syncthreads();
+
+        typename M::Frag xf[2];
+#pragma unroll
+        for (int kk = 0; kk < 2; kk++)
+            xf[kk] = M::gather(x_lds + (32 * kk + 8 * lg) * TileV::kLd + pc, TileV::kLd);
+        typename M::Frag sf[NP / 32];
+#pragma unroll
+        for (int kk = 0; kk < NP / 32; kk++) {
+            const f32x4 u = acc[2 * kk], v = acc[2 * kk + 1];
+            sf[kk] = M::pack(f32x8{u[0], u[1], u[2], u[3], v[0], v[1], v[2], v[3]});
+        }
+#pragma unroll
+        for (int it = 0; it < 4; it++) {
+            f32x4 o = {0, 0, 0, 0};
+            const T* const cr = q_lds + (16 * it + lr) * TileK::kLd + 4 * lg;
+#pragma unroll
+            for (int kk = 0; kk < NP / 32; kk++)
+                o = M::mma(M::load_2x4(cr + 32 * kk, cr + 32 * kk + 16), sf[kk], o);
+#pragma unroll
+            for (int r = 0; r < 4; r++) o[r] *= exp2_hw(c_lds[16 * it + 4 * lg + r].x);
+            if (!scalar) {
+#pragma unroll
+                for (int kk = 0; kk <= it / 2; kk++)
+                    o = M::mma(M::load(m_lds + (16 * it + lr) * TileV::kLd + 32 * kk + 8 * lg), xf[kk], o);
+            } else {
+                // An infinite or NaN x must not meet the zeros of the scores of earlier rows.
+                for (int r = 0; r < 4; r++) {
+                    const int i = 16 * it + 4 * lg + r;
+                    for (int j = 0; j <= i; j++)
+                        o[r] += widen(m_lds[i * TileV::kLd + j]) * widen(x_lds[j * TileV::kLd + pc]);
+                }
+            }
+#pragma unroll
+            for (int r = 0; r < 4; r++) {
+                const int i = 16 * it + 4 * lg + r;
+                if (i < rows && pc < vcols)
+                    yb[(int64_t(ck) * kHeadChunk + i) * yt + pg] =
+                        narrow<T>(o[r] + skip * widen(x_lds[i * TileV::kLd + pc]));
+            }
+        }
+
+        const f32x2 cq = c_lds[63];
+        const float decay = exp2_hw(cq.x);
+#pragma unroll
+        for (int nt = 0; nt < NP / 16; nt++) acc[nt] *= decay;
+        if (!scalar) {
+#pragma unroll
+            for (int kk = 0; kk < 2; kk++) {
+                const int j0 = 32 * kk + 8 * lg;
+                f32x8 wv = M::unpack(xf[kk]);
+#pragma unroll
+                for (int e = 0; e < 8; e++) wv[e] *= exp2_hw(c_diff(cq, c_lds[j0 + e])) * s_lds[j0 + e];
+                typename M::Frag w[M::kWide];
+                M::split(wv, w);
+#pragma unroll
+                for (int nt = 0; nt < NP / 16; nt++)
+                    acc[nt] = mma_wide<T>(M::gather(b_lds + j0 * TileK::kLd + 16 * nt + lr, TileK::kLd), w, acc[nt]);
+            }
+        } else {
+            for (int j = 0; j < 64; j++) {
+                const float wx = exp2_hw(c_diff(cq, c_lds[j])) * s_lds[j] * widen(x_lds[j * TileV::kLd + pc]);
+#pragma unroll
+                for (int nt = 0; nt < NP / 16; nt++)
+#pragma unroll
+                    for (int r = 0; r < 4; r++)
+                        acc[nt][r] += wx * widen(b_lds[j * TileK::kLd + 16 * nt + 4 * lg + r]);
+            }
+        }
+    }
+    if (p.nseg == 1 && p.last && pg < p.P)
+#pragma unroll
+        for (int nt = 0; nt < NP / 16; nt++)
+#pragma unroll
+            for (int r = 0; r < 4; r++) {
+                const int n = 16 * nt + 4 * lg + r;
+                if (n < p.N) p.last[(bh * p.P + pg) * p.N + n] = acc[nt][r];
+            }
+}
+
+// Gradients of one chunk for the heads of one head block of a group.
+//
+// With Q the adjoint of the state after the chunk, S the state before it,
+// G_ij = dy_i . x_j and R_ij = L_ij G_ij s_j:
+//     dC_i = sum_j R_ij B_j + exp(c_i) S^T dy_i            (summed over heads)
+//     dB_j = sum_i R_ij C_i + s_j exp(c_63 - c_j) Q^T x_j  (summed over heads)
+//     dx_j = s_j (sum_i L_ij (C_i . B_j) dy_i + exp(c_63 - c_j) Q B_j) + D dy_j
+// The gradient of log a_t is what flows past step t, from steps j < t and the
+// state S to steps i >= t and the adjoint Q.  With W_ij = L_ij (C_i . B_j) G_ij s_j,
+// Y_i = exp(c_i) C_i . S^T dy_i and X_j = s_j exp(c_63 - c_j) B_j . Q^T x_j:
+//     dlog_t = sum_{i >= t > j} W_ij + sum_{i >= t} Y_i + sum_{j < t} X_j + exp(c_63) <Q, S>
+// The first sum is that over i >= t of the rows' sums less the columns' sums of
+// W below its diagonal (the diagonal, where W is largest, would only cancel).
+// These feed fp32 outputs, so their products keep S and Q as three bf16 parts;
+// R, the scores and the Q of dx, which only feed outputs of the inputs' type,
+// are rounded.
+//
+// Wave w owns rows 16 w.. of the score tiles, 16 NW columns n of dB and dC
+// (accumulated over heads in registers) and 16 columns of dx.
+template <typename T, int NP>
+__global__ __launch_bounds__(256) void head_grad(HeadParams p) {
+    using M = Mat<T>;
+    using TileK = Tile<T, NP>;
+    using TileV = Tile<T, kHeadSlab>;
+    constexpr int NW = NP / 64;
+    extern __shared__ __align__(16) float smem[];
+    T* const b_lds = reinterpret_cast<T*>(smem);
+    T* const q_lds = b_lds + TileK::kElems;
+    T* const x_lds = q_lds + TileK::kElems;
+    T* const dy_lds = x_lds + TileV::kElems;
+    T* const m_lds = dy_lds + TileV::kElems;   // L_ij (C_i . B_j) as [j][i]
+    T* const r_lds = m_lds + TileV::kElems;    // R_ij as [j][i]
+    f32x2* const c_lds = reinterpret_cast<f32x2*>(r_lds + TileV::kElems);
+    float* const s_lds = reinterpret_cast<float*>(c_lds + 64);
+    float* const row_lds = s_lds + 64;         // sum_{j < i} W_ij
+    float* const diag_lds = row_lds + 64;      // W_ii / s_i
+    float* const col_lds = diag_lds + 64;      // [wave][j] sum_{i > j} W_ij / s_j
+    float* const yin_lds = col_lds + 256;      // [wave][i] share of Y_i
+    float* const xin_lds = yin_lds + 256;      // [wave][j] share of X_j / s_j
+    float* const dot_lds = xin_lds + 256;      // [wave] <Q, S>, [4 + wave] sum of G_ii
+
+    const uint32_t piece = piece_of(blockIdx.x, gridDim.x);
+    const int hb = int(piece % uint32_t(p.blocks));
+    uint32_t rest = piece / uint32_t(p.blocks);
+    const int g = int(rest % uint32_t(p.G));
+    rest /= uint32_t(p.G);
+    const int ck = int(rest % uint32_t(p.chunks));
+    const int64_t bi = rest / uint32_t(p.chunks);
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, lr = lane & 15, lg = lane >> 4;
+    const int pc = 16 * wave + lr;
+    const int64_t t0 = int64_t(ck) * kHeadChunk;
+    const int rows = chunk_rows(p, ck), per_group = p.H / p.G;
+    const int h_first = g * per_group + hb * p.per_block;
+    const int h_last = min(h_first + p.per_block, (g + 1) * per_group);
+    const int64_t dyt = int64_t(p.H) * p.P;
+
+    {
+        TileK tb, tc;
+        tb.load(static_cast<const T*>(p.B) + bi * p.Bb + t0 * p.Bt + int64_t(g) * p.N, p.Bt, rows, p.N);
+        tc.load(static_cast<const T*>(p.C) + bi * p.Cb + t0 * p.Ct + int64_t(g) * p.N, p.Ct, rows, p.N);
+        tb.store(b_lds);
+        tc.store(q_lds);
+    }
+    __syncthreads();
+    f32x4 cb[4];   // C_i . B_j, rows i = 16 wave + 4 lg + r, columns j = 16 jt + lr
+#pragma unroll
+    for (int jt = 0; jt < 4; jt++) {
+        cb[jt] = f32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int kk = 0; kk < NP / 32; kk++)
+            cb[jt] = M::mma(M::load(q_lds + (16 * wave + lr) * TileK::kLd + 32 * kk + 8 * lg),
+                            M::load(b_lds + (16 * jt + lr) * TileK::kLd + 32 * kk + 8 * lg), cb[jt]);
+    }
+    const int n0 = 16 * NW * wave + lr;   // this lane's column n of the wave's first tile
+    f32x4 db[4][NW], dc[4][NW];
+#pragma unroll
+    for (int it = 0; it < 4; it++)
+#pragma unroll
+        for (int nt = 0; nt < NW; nt++) db[it][nt] = dc[it][nt] = f32x4{0, 0, 0, 0};
+
+    TileV tx, ty;
+    float dl;
+    auto fetch = [&](int h, int slab) {
+        const int64_t col = int64_t(h) * p.P + slab * kHeadSlab;
+        const int vcols = p.P - slab * kHeadSlab;
+        tx.load(static_cast<const T*>(p.x) + bi * p.xb + t0 * p.xt + col, p.xt, rows, vcols);
+        ty.load(static_cast<const T*>(p.dy) + (bi * p.L + t0) * dyt + col, dyt, rows, vcols);
+        dl = gate_load<T>(p, bi, h, ck);
+    };
+    fetch(h_first, 0);
+    for (int h = h_first; h < h_last; h++) {
+        const int64_t bh = bi * p.H + h;
+        const float a2 = a2_from_alog(p.A_log[h]), bias = p.bias ? p.bias[h] : 0.0f, skip = p.D[h];
+        float to_sum = 0.0f, from_sum = 0.0f, w_sum = 0.0f, dot_sum = 0.0f, d_sum = 0.0f;   // wave 0, lane t
+        Gate gt{};
+        for (int slab = 0; slab < p.slabs; slab++) {
+            __syncthreads();
+            tx.store(x_lds);
+            ty.store(dy_lds);
+            if (wave == 0) {
+                gt = make_gate(dl, bias, a2, p.softplus, lane < rows);
+                c_lds[lane] = gt.c;
+                s_lds[lane] = gt.step;
+            }
+            __syncthreads();
+            if (slab + 1 < p.slabs) fetch(h, slab + 1);
+            else if (h + 1 < h_last) fetch(h + 1, 0);
+
+            const float* const s_at = p.chunk_s + ((bh * p.slabs + slab) * p.chunks + ck) * (NP * 64);
+            const float* const q_at = p.chunk_q + ((bh * p.slabs + slab) * p.chunks + ck) * (NP * 64);
+            const f32x2 cq = c_lds[63];
+
+            // Scores.
+            {
+                f32x4 row_sum = {0, 0, 0, 0};
+                float diag = 0.0f;
+#pragma unroll
+                for (int jt = 0; jt < 4; jt++) {
+                    const int j = 16 * jt + lr;
+                    float col = 0.0f;
+                    f32x4 gs = {0, 0, 0, 0}, ms = {0, 0, 0, 0}, rs = {0, 0, 0, 0};
+                    if (jt <= wave) {
+#pragma unroll
+                        for (int kk = 0; kk < 2; kk++)
+                            gs = M::mma(M::load(dy_lds + (16 * wave + lr) * TileV::kLd + 32 * kk + 8 * lg),
+                                        M::load(x_lds + j * TileV::kLd + 32 * kk + 8 * lg), gs);
+                        const f32x2 cj = c_lds[j];
+                        const float sj = s_lds[j];
+#pragma unroll
+                        for (int r = 0; r < 4; r++) {
+                            const int i = 16 * wave + 4 * lg + r;
+                            if (j <= i) {
+                                const float w = exp2_hw(c_diff(c_lds[i], cj));
+                                ms[r] = w * cb[jt][r];
+                                rs[r] = w * gs[r] * sj;
+                                const float pr = ms[r] * gs[r];
+                                if (j < i) {
+                                    col += pr;
+                                    row_sum[r] += pr * sj;
+                                } else {
+                                    diag_lds[j] = pr;
+                                    diag += gs[r];
+                                }
+                            }
+                        }
+                    }
+                    if (jt <= (wave | 1)) {
+                        store4(m_lds + j * TileV::kLd + 16 * wave + 4 * lg, ms);
+                        store4(r_lds + j * TileV::kLd + 16 * wave + 4 * lg, rs);
+                    }
+                    col = sum_groups4(col);
+                    if (lg == 0) col_lds[64 * wave + j] = col;
+                }
+#pragma unroll
+                for (int r = 0; r < 4; r++) {
+                    const float v = sum_lanes16(row_sum[r]);
+                    if (lr == 0) row_lds[16 * wave + 4 * lg + r] = v;
+                }
+                diag = sum_wave(diag);
+                if (lane == 0) dot_lds[4 + wave] = diag;
+            }
+            __syncthreads();
+
+            // dC, dB and the state terms.
+            float dot = 0.0f;
+            float yin[4][4], xin[4][4];
+#pragma unroll
+            for (int it = 0; it < 4; it++)
+#pragma unroll
+                for (int r = 0; r < 4; r++) yin[it][r] = xin[it][r] = 0.0f;
+#pragma unroll
+            for (int nt = 0; nt < NW; nt++) {
+                const int n = n0 + 16 * nt;
+                f32x8 sv[2], qv[2];
+#pragma unroll
+                for (int kk = 0; kk < 2; kk++) {
+                    sv[kk] = Mat<float>::load(s_at + n * 64 + 32 * kk + 8 * lg);
+                    qv[kk] = Mat<float>::load(q_at + n * 64 + 32 * kk + 8 * lg);
+#pragma unroll
+                    for (int e = 0; e < 8; e++) dot += sv[kk][e] * qv[kk][e];
+                }
+                typename M::Frag sf[2][M::kWide], qf[2][M::kWide], bf[2], cf[2];
+#pragma unroll
+                for (int kk = 0; kk < 2; kk++) {
+                    M::split(sv[kk], sf[kk]);
+                    M::split(qv[kk], qf[kk]);
+                    bf[kk] = M::gather(b_lds + (32 * kk + 8 * lg) * TileK::kLd + n, TileK::kLd);
+                    cf[kk] = M::gather(q_lds + (32 * kk + 8 * lg) * TileK::kLd + n, TileK::kLd);
+                }
+#pragma unroll
+                for (int it = 0; it < 4; it++) {
+                    f32x4 u = {0, 0, 0, 0}, v = {0, 0, 0, 0};
+#pragma unroll
+                    for (int kk = 0; kk < 2; kk++) {
+                        u = mma_wide<T>(M::load(dy_lds + (16 * it + lr) * TileV::kLd + 32 * kk + 8 * lg), sf[kk], u);
+                        v = mma_wide<T>(M::load(x_lds + (16 * it + lr) * TileV::kLd + 32 * kk + 8 * lg), qf[kk], v);
+                    }
+#pragma unroll
+                    for (int r = 0; r < 4; r++) {
+                        const int i = 16 * it + 4 * lg + r;
+                        const float ui = u[r] * exp2_hw(c_lds[i].x), vi = v[r] * exp2_hw(c_diff(cq, c_lds[i]));
+                        yin[it][r] += ui * widen(q_lds[i * TileK::kLd + n]);
+                        xin[it][r] += vi * widen(b_lds[i * TileK::kLd + n]);
+                        dc[it][nt][r] += ui;
+                        db[it][nt][r] += vi * s_lds[i];
+                    }
+#pragma unroll
+                    for (int kk = 0; kk <= it / 2; kk++)
+                        dc[it][nt] = M::mma(M::gather(r_lds + (32 * kk + 8 * lg) * TileV::kLd + 16 * it + lr, TileV::kLd),
+                                            bf[kk], dc[it][nt]);
+#pragma unroll
+                    for (int kk = it / 2; kk < 2; kk++)
+                        db[it][nt] = M::mma(M::load(r_lds + (16 * it + lr) * TileV::kLd + 32 * kk + 8 * lg), cf[kk],
+                                            db[it][nt]);
+                }
+            }
+#pragma unroll
+            for (int it = 0; it < 4; it++)
+#pragma unroll
+                for (int r = 0; r < 4; r++) {
+                    const float a = sum_lanes16(yin[it][r]), b = sum_lanes16(xin[it][r]);
+                    if (lr == 0) {
+                        yin_lds[64 * wave + 16 * it + 4 * lg + r] = a;
+                        xin_lds[64 * wave + 16 * it + 4 * lg + r] = b;
+                    }
+                }
+            dot = sum_wave(dot);
+            if (lane == 0) dot_lds[wave] = dot;
+
+            // dx.
+            typename M::Frag qb[NP / 32], df[2];
+#pragma unroll
+            for (int kk = 0; kk < NP / 32; kk++) {
+                f32x8 v;
+#pragma unroll
+                for (int e = 0; e < 8; e++) v[e] = q_at[(32 * kk + 8 * lg + e) * 64 + pc];
+                qb[kk] = M::pack(v);
+            }
+#pragma unroll
+            for (int kk = 0; kk < 2; kk++)
+                df[kk] = M::gather(dy_lds + (32 * kk + 8 * lg) * TileV::kLd + pc, TileV::kLd);
+            const bool inside = pc < p.P - slab * kHeadSlab;
+            T* const dx = static_cast<T*>(p.dx) + (bi * p.L + t0) * dyt + int64_t(h) * p.P + slab * kHeadSlab + pc;
+#pragma unroll
+            for (int jt = 0; jt < 4; jt++) {
+                f32x4 o = {0, 0, 0, 0};
+#pragma unroll
+                for (int kk = 0; kk < NP / 32; kk++)
+                    o = M::mma(M::load(b_lds + (16 * jt + lr) * TileK::kLd + 32 * kk + 8 * lg), qb[kk], o);
+#pragma unroll
+                for (int r = 0; r < 4; r++) o[r] *= exp2_hw(c_diff(cq, c_lds[16 * jt + 4 * lg + r]));
+#pragma unroll
+                for (int kk = jt / 2; kk < 2; kk++)
+                    o = M::mma(M::load(m_lds + (16 * jt + lr) * TileV::kLd + 32 * kk + 8 * lg), df[kk], o);
+#pragma unroll
+                for (int r = 0; r < 4; r++) {
+                    const int j = 16 * jt + 4 * lg + r;
+                    if (j < rows && inside)
+                        dx[j * dyt] = narrow<T>(o[r] * s_lds[j] + skip * widen(dy_lds[j * TileV::kLd + pc]));
+                }
+            }
+            __syncthreads();
+            if (wave == 0) {
+                float yi = 0.0f, xi = 0.0f, ci = 0.0f;
+#pragma unroll
+                for (int w = 0; w < 4; w++) {
+                    yi += yin_lds[64 * w + lane];
+                    xi += xin_lds[64 * w + lane];
+                    ci += col_lds[64 * w + lane];
+                    dot_sum += dot_lds[w];
+                    d_sum += dot_lds[4 + w];
+                }
+                to_sum += row_lds[lane] - gt.step * ci + yi;
+                from_sum += gt.step * xi;
+                w_sum += diag_lds[lane] + ci + xi;
+            }
+        }
+        if (wave == 0) {
+            float to = to_sum, from = from_sum;   // sums over steps >= t, and < t
+#pragma unroll
+            for (int m = 1; m < 64; m <<= 1) {
+                const float down = __shfl_down(to, m), up = __shfl_up(from, m);
+                to += lane + m < 64 ? down : 0.0f;
+                from += lane >= m ? up : 0.0f;
+            }
+            from = __shfl_up(from, 1);
+            const float dlog = to + (lane > 0 ? from : 0.0f) + exp2_hw(c_lds[63].x) * dot_sum;
+            const float a = a2 * kLn2;
+            float dstep = a * dlog + w_sum;   // w_sum lacks the step: it is what it is the gradient of
+            if (p.softplus) dstep *= rcp_hw(1.0f + exp2_hw(-gt.raw * kLog2e));
+            if (lane < rows)
+                static_cast<T*>(p.ddelta)[(bi * p.L + t0 + lane) * p.H + h] = narrow<T>(dstep);
+            const float da = sum_wave(lane < rows ? dlog * gt.step * a : 0.0f);
+            const float dbias = sum_wave(lane < rows ? dstep : 0.0f);
+            if (lane == 0) {
+                const int64_t at = (bi * p.chunks + ck) * p.H + h, one = p.b * p.chunks * p.H;
+                p.partial[at] = da;
+                p.partial[one + at] = dbias;
+                p.partial[2 * one + at] = d_sum;
+            }
+        }
+    }
+#pragma unroll
+    for (int it = 0; it < 4; it++)
+#pragma unroll
+        for (int nt = 0; nt < NW; nt++)
+#pragma unroll
+            for (int r = 0; r < 4; r++) {
+                const int i = 16 * it + 4 * lg + r, n = n0 + 16 * nt;
+                if (i >= rows || n >= p.N) continue;
+                const int64_t at = ((bi * p.L + t0 + i) * p.G + g) * p.N + n;
+                if (p.blocks == 1) {
+                    static_cast<T*>(p.dB)[at] = narrow<T>(db[it][nt][r]);
+                    static_cast<T*>(p.dC)[at] = narrow<T>(dc[it][nt][r]);
+                } else {
+                    const int64_t one = p.b * p.L * p.G * p.N;
+                    p.dbc[hb * one + at] = db[it][nt][r];
+                    p.dbc[(p.blocks + hb) * one + at] = dc[it][nt][r];
+                }
+            }
+}
+
+// dB and dC from the head blocks' shares, in block order.
+template <typename T>
+__global__ __launch_bounds__(256) void head_sum_blocks(HeadParams p) {
+    const int64_t one = p.b * p.L * p.G * p.N;
+    for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < 2 * one; i += int64_t(gridDim.x) * 256) {
+        const bool second = i >= one;
+        const int64_t at = second ? i - one : i;
+        const float* const src = p.dbc + (second ? p.blocks * one : 0) + at;
+        float v = src[0];
+        for (int k = 1; k < p.blocks; k++) v += src[k * one];
+        static_cast<T*>(second ? p.dC : p.dB)[at] = narrow<T>(v);
+    }
+}
+
+// dA_log, ddelta_bias and dD from the chunks' shares: one workgroup per head
+// and output, each thread every 256th chunk, then a tree.
+__global__ __launch_bounds__(256) void head_sum_chunks(HeadParams p) {
+    __shared__ float part[4];
+    const int h = int(blockIdx.x) % p.H, k = int(blockIdx.x) / p.H;
+    const int64_t count = p.b * p.chunks;
+    const float* const src = p.partial + k * count * p.H + h;
+    float v = 0.0f;
+    for (int64_t i = threadIdx.x; i < count; i += 256) v += src[i * p.H];
+    v = sum_wave(v);
+    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
+    __syncthreads();
+    float* const out = k == 0 ? p.dA_log : k == 1 ? p.dbias : p.dD;
+    if (threadIdx.x == 0 && out) out[h] = (part[0] + part[1]) + (part[2] + part[3]);
+}
+
+// One decode step.  A row (b, h, p) of the state is N consecutive values:
+// LPR lanes take 4 of them at a time (VEC) or one, and share the readout's sum.
+template <typename T, int LPR, bool VEC>
+__global__ __launch_bounds__(256) void head_step(float* state, const T* x, const T* dt, const float* A_log, const T* B,
+                                                 const T* C, const float* D, const float* dt_bias, int use_softplus,
+                                                 T* y, int64_t b, int H, int P, int N, int G) {
+    const int64_t row = (int64_t(blockIdx.x) * 256 + threadIdx.x) / LPR, rows = b * H * P;
+    const int sub = threadIdx.x % LPR;
+    if (row >= rows) return;   // whole groups of LPR lanes leave together
+    const int64_t bh = row / P, bi = bh / H;
+    const int h = int(bh % H);
+    const int64_t bg = (bi * G + h / (H / G)) * N;
+    const float step = step_size(Elem<T>::load(dt, bh), dt_bias ? dt_bias[h] : 0.0f, use_softplus);
+    const float a = exp2_hw(step * a2_from_alog(A_log[h]));
+    const float xv = Elem<T>::load(x, row), sx = step * xv;
+    float* const s = state + row * N;
+    float sum = 0.0f;
+    constexpr int V = VEC ? 4 : 1;
+    for (int n = sub * V; n < N; n += LPR * V) {
+        float v[V];
+        if constexpr (VEC) {
+            const f32x4 w = *reinterpret_cast<const f32x4*>(s + n);
+#pragma unroll
+            for (int e = 0; e < V; e++) v[e] = w[e];
+        } else {
+            v[0] = s[n];
+        }
+#pragma unroll
+        for (int e = 0; e < V; e++) {
+            v[e] = a * v[e] + sx * Elem<T>::load(B, bg + n + e);
+            sum += v[e] * Elem<T>::load(C, bg + n + e);
+        }
+        if constexpr (VEC) *reinterpret_cast<f32x4*>(s + n) = f32x4{v[0], v[1], v[2], v[3]};
+        else s[n] = v[0];
+    }
+#pragma unroll
+    for (int m = 1; m < LPR; m <<= 1) sum += __shfl_xor(sum, m);
+    if (sub == 0) Elem<T>::store(y, row, sum + D[h] * xv);
+}
+
+// LDS bytes of the kernels above.
+template <typename T, int NP>
+constexpr size_t head_states_lds() {
+    return (Tile<T, NP>::kElems + Tile<T, kHeadSlab>::kElems) * sizeof(T) + 3 * 64 * sizeof(float);
+}
+template <typename T, int NP>
+constexpr size_t head_out_lds() {
+    return (2 * Tile<T, NP>::kElems + 2 * Tile<T, kHeadSlab>::kElems) * sizeof(T) + 3 * 64 * sizeof(float);
+}
+
+template <typename T, int NP>
+constexpr size_t head_grad_lds() {
+    return (2 * Tile<T, NP>::kElems + 4 * Tile<T, kHeadSlab>::kElems) * sizeof(T) + (5 * 64 + 3 * 256 + 8) * sizeof(float);
+}
+
+}  // namespace ss

@@ -1,0 +1,355 @@
+// head_scan.hip -- host side of the head-wise selective scan (ss_block.h):
+// argument checks, the split of the sequence, workspace layout and launches.
+#include "block_host.h"
+#include "head_kernels.h"
+
+namespace {
+
+using namespace ss_block;
+using ss::HeadParams;
+using ss::StateMode;
+
+constexpr int64_t kMaxLength = (int64_t(1) << 31) - 1024;
+constexpr int64_t kMaxPieces = int64_t(1) << 24;   // workgroups of 256 threads in one launch
+
+struct Shape {
+    int64_t b, L, H, P, N, G;
+    int64_t slabs() const { return (P + ss::kHeadSlab - 1) / ss::kHeadSlab; }
+    int64_t chunks() const { return (L + ss::kHeadChunk - 1) / ss::kHeadChunk; }
+};
+
+int check_shape(const Shape& s, int dtype) {
+    if (!sizes_ok({s.b, s.L, s.H, s.P}) || !sizes_ok({s.b, s.L, s.G, s.N}) || !sizes_ok({s.b, s.H, s.P, s.N}))
+        return SS_ERR_SHAPE;
+    if (s.H % s.G != 0 || s.L > kMaxLength) return SS_ERR_SHAPE;
+    if (!dtype_ok(dtype)) return SS_ERR_DTYPE;
+    if (s.P > SS_MAX_HEAD_DIM || s.N > SS_MAX_HEAD_STATE) return SS_ERR_UNSUPPORTED;
+    if (!sizes_ok({s.b, s.H, s.slabs(), s.chunks()}) || s.b * s.H * s.slabs() * s.chunks() >= kMaxPieces)
+        return SS_ERR_SHAPE;
+    return SS_OK;
+}
+
+// The state's rows as the kernels pad them.
+int64_t padded_state(int64_t N, bool grad) { return N <= 32 && !grad ? 32 : N <= 64 ? 64 : 128; }
+
+// Segments of the sequence that are walked over at the same time.  A walk over
+// one (row, head, slab) is one workgroup; where those are fewer than twice the
+// compute units, the sequence is split so that they are not, down to two
+// chunks a segment, at the cost of a first pass over x and B for the states
+// at the segments' starts.
+constexpr int64_t kWantedPieces = 512;
+
+int64_t segment_chunks(const Shape& s) {
+    const int64_t base = s.b * s.H * s.slabs(), chunks = s.chunks();
+    const int64_t segs = std::max<int64_t>(1, std::min((kWantedPieces + base - 1) / base, chunks / 2));
+    return (chunks + segs - 1) / segs;
+}
+
+int64_t segments(const Shape& s) { return (s.chunks() + segment_chunks(s) - 1) / segment_chunks(s); }
+
+// Heads of a group whose shares of dB and dC one workgroup of the backward
+// adds up: all of them, unless that leaves fewer than 1024 workgroups.
+int64_t heads_per_block(const Shape& s) {
+    const int64_t base = s.b * s.chunks() * s.G, per_group = s.H / s.G;
+    const int64_t blocks = std::max<int64_t>(1, std::min((1024 + base - 1) / base, per_group));
+    return (per_group + blocks - 1) / blocks;
+}
+
+struct Workspace {
+    size_t seg_state, seg_decay, chunk_s, chunk_q, partial, dbc, total;
+};
+
+Workspace layout(const Shape& s, bool grad) {
+    const size_t np = size_t(padded_state(s.N, grad)) * 64 * sizeof(float);
+    const size_t walks = size_t(s.b * s.H * s.slabs()), nseg = size_t(segments(s));
+    Workspace w{};
+    size_t at = 0;
+    auto take = [&](size_t& field, size_t bytes) {
+        field = at;
+        at += round256(bytes);
+    };
+    take(w.seg_state, nseg > 1 ? walks * nseg * np : 0);
+    take(w.seg_decay, nseg > 1 ? size_t(s.b * s.H) * nseg * sizeof(float) : 0);
+    if (grad) {
+        const int64_t per_group = s.H / s.G, per = heads_per_block(s), blocks = (per_group + per - 1) / per;
+        take(w.chunk_s, walks * size_t(s.chunks()) * np);
+        take(w.chunk_q, walks * size_t(s.chunks()) * np);
+        take(w.partial, 3 * size_t(s.b * s.chunks() * s.H) * sizeof(float));
+        take(w.dbc, blocks > 1 ? 2 * size_t(blocks) * size_t(s.b * s.L * s.G * s.N) * sizeof(float) : 0);
+    }
+    w.total = at;
+    return w;
+}
+
+struct Strides {
+    int64_t xb, xt, db, dt, Bb, Bt, Cb, Ct;
+};
+
+Strides strides_of(const Shape& s, const int64_t* given) {
+    if (given) return {given[0], given[1], given[2], given[3], given[4], given[5], given[6], given[7]};
+    return {s.L * s.H * s.P, s.H * s.P, s.L * s.H, s.H, s.L * s.G * s.N, s.G * s.N, s.L * s.G * s.N, s.G * s.N};
+}
+
+// Elements from a strided tensor's first to past its last; -1 where that is not below 2^46.
+int64_t extent(const Shape& s, int64_t sb, int64_t st, int64_t inner) {
+    if (sb < 0 || st < 0 || sb > kMaxElems / s.b || st > kMaxElems / s.L) return -1;
+    const int64_t n = (s.b - 1) * sb + (s.L - 1) * st + inner;
+    return n <= kMaxElems ? n : -1;
+}
+
+HeadParams params_of(const Shape& s, const Strides& st, void* ws, bool grad) {
+    HeadParams p{};
+    p.b = s.b;
+    p.L = s.L;
+    p.H = int(s.H);
+    p.P = int(s.P);
+    p.N = int(s.N);
+    p.G = int(s.G);
+    p.slabs = int(s.slabs());
+    p.chunks = int(s.chunks());
+    p.seg_chunks = int(segment_chunks(s));
+    p.nseg = int(segments(s));
+    p.xb = st.xb;
+    p.xt = st.xt;
+    p.deltab = st.db;
+    p.deltat = st.dt;
+    p.Bb = st.Bb;
+    p.Bt = st.Bt;
+    p.Cb = st.Cb;
+    p.Ct = st.Ct;
+    const Workspace w = layout(s, grad);
+    char* const at = static_cast<char*>(ws);
+    p.seg_state = reinterpret_cast<float*>(at + w.seg_state);
+    p.seg_decay = reinterpret_cast<float*>(at + w.seg_decay);
+    p.chunk_s = reinterpret_cast<float*>(at + w.chunk_s);
+    p.chunk_q = reinterpret_cast<float*>(at + w.chunk_q);
+    p.partial = reinterpret_cast<float*>(at + w.partial);
+    p.dbc = reinterpret_cast<float*>(at + w.dbc);
+    p.per_block = int(heads_per_block(s));
+    p.blocks = int((s.H / s.G + p.per_block - 1) / p.per_block);
+    return p;
+}
+
+template <typename T, int NP, bool REV>
+void carry_segments(const HeadParams& p, hipStream_t st) {
+    const unsigned walks = unsigned(p.b * p.H * p.slabs);
+    ss::head_states<T, NP, REV, StateMode::Local><<<walks * p.nseg, 256, ss::head_states_lds<T, NP>(), st>>>(p);
+    ss::head_carry<NP, REV><<<walks * (NP * 64 / 256), 256, 0, st>>>(p);
+}
+
+template <typename T, int NP>
+int run_fwd(const HeadParams& p, hipStream_t st) {
+    const unsigned walks = unsigned(p.b * p.H * p.slabs);
+    if (p.nseg > 1) carry_segments<T, NP, false>(p, st);
+    ss::head_out<T, NP><<<walks * p.nseg, 256, ss::head_out_lds<T, NP>(), st>>>(p);
+    return status(hipGetLastError());
+}
+
+template <typename T, int NP>
+int run_bwd(HeadParams p, hipStream_t st) {
+    const unsigned walks = unsigned(p.b * p.H * p.slabs);
+    p.last = nullptr;
+    if (p.nseg > 1) carry_segments<T, NP, false>(p, st);
+    ss::head_states<T, NP, false, StateMode::Chunks><<<walks * p.nseg, 256, ss::head_states_lds<T, NP>(), st>>>(p);
+    if (p.nseg > 1) carry_segments<T, NP, true>(p, st);
+    ss::head_states<T, NP, true, StateMode::Chunks><<<walks * p.nseg, 256, ss::head_states_lds<T, NP>(), st>>>(p);
+    const unsigned grid = unsigned(p.b * p.chunks * p.G * p.blocks);
+    ss::head_grad<T, NP><<<grid, 256, ss::head_grad_lds<T, NP>(), st>>>(p);
+    if (p.blocks > 1) {
+        const int64_t items = 2 * p.b * p.L * p.G * p.N;
+        ss::head_sum_blocks<T><<<unsigned(std::min<int64_t>((items + 255) / 256, 1 << 20)), 256, 0, st>>>(p);
+    }
+    ss::head_sum_chunks<<<3 * p.H, 256, 0, st>>>(p);
+    return status(hipGetLastError());
+}
+
+template <typename T>
+int dispatch_fwd(const HeadParams& p, hipStream_t st) {
+    switch (padded_state(p.N, false)) {
+        case 32: return run_fwd<T, 32>(p, st);
+        case 64: return run_fwd<T, 64>(p, st);
+        default: return run_fwd<T, 128>(p, st);
+    }
+}
+
+template <typename T>
+int dispatch_bwd(const HeadParams& p, hipStream_t st) {
+    return padded_state(p.N, true) == 64 ? run_bwd<T, 64>(p, st) : run_bwd<T, 128>(p, st);
+}
+
+template <typename T, bool VEC>
+void launch_step(int lpr, int64_t rows, hipStream_t st, float* state, const T* x, const T* dt, const float* A_log,
+                 const T* B, const T* C, const float* D, const float* bias, int softplus, T* y, int64_t b, int H,
+                 int P, int N, int G) {
+    auto run = [&](auto kernel, int lanes) {
+        kernel<<<unsigned((rows * lanes + 255) / 256), 256, 0, st>>>(state, x, dt, A_log, B, C, D, bias, softplus, y, b,
+                                                                     H, P, N, G);
+    };
+    if (lpr <= 4) run(ss::head_step<T, 4, VEC>, 4);
+    else if (lpr <= 8) run(ss::head_step<T, 8, VEC>, 8);
+    else if (lpr <= 16) run(ss::head_step<T, 16, VEC>, 16);
+    else run(ss::head_step<T, 32, VEC>, 32);
+}
+
+template <typename T>
+int run_step(float* state, const void* x, const void* dt, const float* A_log, const void* B, const void* C,
+             const float* D, const float* bias, int softplus, void* y, const Shape& s, hipStream_t st) {
+    // Lanes that cover a row of the state once, 16 bytes each where the rows allow it.
+    const bool vec = s.N % 4 == 0 && aligned(state, 16);
+    const int lpr = int(vec ? s.N / 4 : s.N);
+    auto go = [&](auto v) {
+        launch_step<T, decltype(v)::value>(lpr, s.b * s.H * s.P, st, state, static_cast<const T*>(x),
+                                           static_cast<const T*>(dt), A_log, static_cast<const T*>(B),
+                                           static_cast<const T*>(C), D, bias, softplus, static_cast<T*>(y), s.b,
+                                           int(s.H), int(s.P), int(s.N), int(s.G));
+    };
+    if (vec) go(std::true_type{});
+    else go(std::false_type{});
+    return status(hipGetLastError());
+}
+
+}  // namespace
+
+SS_EXPORT size_t ss_head_scan_fwd_workspace_bytes(int64_t b, int64_t L, int64_t H, int64_t P, int64_t N, int64_t G,
+                                                  int dtype) {
+    const Shape s{b, L, H, P, N, G};
+    return check_shape(s, dtype) == SS_OK ? layout(s, false).total : 0;
+}
+
+SS_EXPORT size_t ss_head_scan_bwd_workspace_bytes(int64_t b, int64_t L, int64_t H, int64_t P, int64_t N, int64_t G,
+                                                  int dtype) {
+    const Shape s{b, L, H, P, N, G};
+    return check_shape(s, dtype) == SS_OK ? layout(s, true).total : 0;
+}
+
+SS_EXPORT int ss_head_scan_fwd(const void* x, const void* delta, const float* A_log, const void* B, const void* C,
+                               const float* D, const float* delta_bias, int delta_softplus,
+                               const float* initial_state, void* y, float* last_state, int64_t b, int64_t L, int64_t H,
+                               int64_t P, int64_t N, int64_t G, int dtype, const int64_t* strides, void* workspace,
+                               size_t workspace_bytes, void* stream) {
+    if (!x || !delta || !A_log || !B || !C || !D || !y) return SS_ERR_NULL;
+    const Shape s{b, L, H, P, N, G};
+    if (const int rc = check_shape(s, dtype)) return rc;
+    const Strides st = strides_of(s, strides);
+    const int64_t ex = extent(s, st.xb, st.xt, H * P), ed = extent(s, st.db, st.dt, H),
+                  eB = extent(s, st.Bb, st.Bt, G * N), eC = extent(s, st.Cb, st.Ct, G * N);
+    if (ex < 0 || ed < 0 || eB < 0 || eC < 0) return SS_ERR_SHAPE;
+    const size_t es = elem_size(dtype);
+    for (const void* p : {x, delta, B, C, static_cast<const void*>(y)})
+        if (!aligned(p, es)) return SS_ERR_ALIGN;
+    for (const float* p : {A_log, D, delta_bias, initial_state, static_cast<const float*>(last_state)})
+        if (!aligned(p, 4)) return SS_ERR_ALIGN;
+    const int64_t ns = b * H * P * N;
+    const Range rh = range_of(initial_state, ns, 4), rl = range_of(last_state, ns, 4);
+    const Range ins[] = {range_of(x, ex, es), range_of(delta, ed, es), range_of(B, eB, es), range_of(C, eC, es),
+                         range_of(A_log, H, 4), range_of(D, H, 4), range_of(delta_bias, H, 4),
+                         same(rh, rl) ? Range{0, 0} : rh};
+    const Range outs[] = {range_of(y, b * L * H * P, es), rl};
+    if (!apart(ins, outs) || overlaps(rh, outs[0])) return SS_ERR_ALIAS;
+    const size_t need = layout(s, false).total;
+    if (need) {
+        if (!workspace || workspace_bytes < need) return SS_ERR_WORKSPACE;
+        if (!aligned(workspace, 256)) return SS_ERR_ALIGN;
+        const Range rw[] = {range_of(workspace, int64_t(need), 1)};
+        if (!apart(ins, rw) || !apart(outs, rw) || overlaps(rh, rw[0])) return SS_ERR_ALIAS;
+    }
+    HeadParams p = params_of(s, st, workspace, false);
+    p.x = x;
+    p.delta = delta;
+    p.A_log = A_log;
+    p.B = B;
+    p.C = C;
+    p.D = D;
+    p.bias = delta_bias;
+    p.softplus = delta_softplus ? 1 : 0;
+    p.h0 = initial_state;
+    p.y = y;
+    p.last = last_state;
+    const hipStream_t hs = static_cast<hipStream_t>(stream);
+    return dtype == SS_BF16 ? dispatch_fwd<uint16_t>(p, hs) : dispatch_fwd<float>(p, hs);
+}
+
+SS_EXPORT int ss_head_scan_bwd(const void* x, const void* delta, const float* A_log, const void* B, const void* C,
+                               const float* D, const float* delta_bias, int delta_softplus,
+                               const float* initial_state, const void* dy, const float* dlast_state, void* dx,
+                               void* ddelta, float* dA_log, void* dB, void* dC, float* dD, float* ddelta_bias,
+                               float* dinitial_state, int64_t b, int64_t L, int64_t H, int64_t P, int64_t N, int64_t G,
+                               int dtype, const int64_t* strides, void* workspace, size_t workspace_bytes,
+                               void* stream) {
+    if (!x || !delta || !A_log || !B || !C || !D || !dy || !dx || !ddelta || !dA_log || !dB || !dC || !dD)
+        return SS_ERR_NULL;
+    const Shape s{b, L, H, P, N, G};
+    if (const int rc = check_shape(s, dtype)) return rc;
+    const Strides st = strides_of(s, strides);
+    const int64_t ex = extent(s, st.xb, st.xt, H * P), ed = extent(s, st.db, st.dt, H),
+                  eB = extent(s, st.Bb, st.Bt, G * N), eC = extent(s, st.Cb, st.Ct, G * N);
+    if (ex < 0 || ed < 0 || eB < 0 || eC < 0) return SS_ERR_SHAPE;
+    const size_t es = elem_size(dtype);
+    for (const void* p : {x, delta, B, C, dy, static_cast<const void*>(dx), static_cast<const void*>(ddelta),
+                          static_cast<const void*>(dB), static_cast<const void*>(dC)})
+        if (!aligned(p, es)) return SS_ERR_ALIGN;
+    for (const float* p : {A_log, D, delta_bias, initial_state, dlast_state, static_cast<const float*>(dA_log),
+                           static_cast<const float*>(dD), static_cast<const float*>(ddelta_bias),
+                           static_cast<const float*>(dinitial_state)})
+        if (!aligned(p, 4)) return SS_ERR_ALIGN;
+    const int64_t ns = b * H * P * N, nx = b * L * H * P, nb = b * L * G * N;
+    const Range ins[] = {range_of(x, ex, es), range_of(delta, ed, es), range_of(B, eB, es), range_of(C, eC, es),
+                         range_of(A_log, H, 4), range_of(D, H, 4), range_of(delta_bias, H, 4),
+                         range_of(initial_state, ns, 4), range_of(dy, nx, es), range_of(dlast_state, ns, 4)};
+    const Range outs[] = {range_of(dx, nx, es), range_of(ddelta, b * L * H, es), range_of(dA_log, H, 4),
+                          range_of(dB, nb, es), range_of(dC, nb, es), range_of(dD, H, 4),
+                          range_of(ddelta_bias, H, 4), range_of(dinitial_state, ns, 4)};
+    if (!apart(ins, outs)) return SS_ERR_ALIAS;
+    const size_t need = layout(s, true).total;
+    if (!workspace || workspace_bytes < need) return SS_ERR_WORKSPACE;
+    if (!aligned(workspace, 256)) return SS_ERR_ALIGN;
+    const Range rw[] = {range_of(workspace, int64_t(need), 1)};
+    if (!apart(ins, rw) || !apart(outs, rw)) return SS_ERR_ALIAS;
+    HeadParams p = params_of(s, st, workspace, true);
+    p.x = x;
+    p.delta = delta;
+    p.A_log = A_log;
+    p.B = B;
+    p.C = C;
+    p.D = D;
+    p.bias = delta_bias;
+    p.softplus = delta_softplus ? 1 : 0;
+    p.h0 = initial_state;
+    p.dy = dy;
+    p.dlast = dlast_state;
+    p.dx = dx;
+    p.ddelta = ddelta;
+    p.dA_log = dA_log;
+    p.dB = dB;
+    p.dC = dC;
+    p.dD = dD;
+    p.dbias = ddelta_bias;
+    p.dh0 = dinitial_state;
+    const hipStream_t hs = static_cast<hipStream_t>(stream);
+    return dtype == SS_BF16 ? dispatch_bwd<uint16_t>(p, hs) : dispatch_bwd<float>(p, hs);
+}
+
+SS_EXPORT int ss_head_state_update(float* state, const void* x, const void* dt, const float* A_log, const void* B,
+                                   const void* C, const float* D, const float* dt_bias, int dt_softplus, void* y,
+                                   int64_t b, int64_t H, int64_t P, int64_t N, int64_t G, int dtype, void* stream) {
+    if (!state || !x || !dt || !A_log || !B || !C || !D || !y) return SS_ERR_NULL;
+    const Shape s{b, 1, H, P, N, G};
+    if (!sizes_ok({b, H, P, N}) || !sizes_ok({b, G, N}) || H % G != 0 || b * H * P >= (int64_t(1) << 28))
+        return SS_ERR_SHAPE;
+    if (!dtype_ok(dtype)) return SS_ERR_DTYPE;
+    if (P > SS_MAX_HEAD_DIM || N > SS_MAX_HEAD_STATE) return SS_ERR_UNSUPPORTED;
+    const size_t es = elem_size(dtype);
+    for (const void* p : {x, dt, B, C, static_cast<const void*>(y)})
+        if (!aligned(p, es)) return SS_ERR_ALIGN;
+    for (const float* p : {static_cast<const float*>(state), A_log, D, dt_bias})
+        if (!aligned(p, 4)) return SS_ERR_ALIGN;
+    const Range ins[] = {range_of(x, b * H * P, es), range_of(dt, b * H, es), range_of(B, b * G * N, es),
+                         range_of(C, b * G * N, es), range_of(A_log, H, 4), range_of(D, H, 4),
+                         range_of(dt_bias, H, 4)};
+    const Range outs[] = {range_of(state, b * H * P * N, 4), range_of(y, b * H * P, es)};
+    if (!apart(ins, outs)) return SS_ERR_ALIAS;
+    const hipStream_t hs = static_cast<hipStream_t>(stream);
+    const int softplus = dt_softplus ? 1 : 0;
+    return dtype == SS_BF16 ? run_step<uint16_t>(state, x, dt, A_log, B, C, D, dt_bias, softplus, y, s, hs)
+                            : run_step<float>(state, x, dt, A_log, B, C, D, dt_bias, softplus, y, s, hs);
+}

@@ -1,0 +1,265 @@
+// norms.hip -- host side of the residual and the gated norm (ss_block.h).
+#include <cmath>
+
+#include "block_host.h"
+#include "norm_kernels.h"
+
+namespace {
+
+using namespace ss_block;
+using ss::NormParams;
+
+constexpr int64_t kMaxRows = (int64_t(1) << 31) - 1;
+
+// Threads and vectors per thread of a row of `gd` channels: a wave up to 1024
+// channels (no barriers), a workgroup beyond; the row stays in registers.
+template <typename F>
+void by_width(int gd, F&& f) {
+    using std::integral_constant;
+    auto go = [&](auto threads, auto vpt) { f(threads, vpt); };
+    if (gd <= 512) go(integral_constant<int, 64>{}, integral_constant<int, 1>{});
+    else if (gd <= 1024) go(integral_constant<int, 64>{}, integral_constant<int, 2>{});
+    else if (gd <= 2048) go(integral_constant<int, 256>{}, integral_constant<int, 1>{});
+    else if (gd <= 4096) go(integral_constant<int, 256>{}, integral_constant<int, 2>{});
+    else if (gd <= 8192) go(integral_constant<int, 256>{}, integral_constant<int, 4>{});
+    else go(integral_constant<int, 1024>{}, integral_constant<int, 2>{});
+}
+
+bool is_wave(int gd) { return gd <= 1024; }
+int block_threads(int gd) { return gd > 8192 ? 1024 : 256; }
+
+unsigned fwd_grid(int64_t units, int gd) {
+    const int64_t wgs = is_wave(gd) ? (units + 3) / 4 : units;
+    return unsigned(std::min<int64_t>(wgs, int64_t(1) << 21));
+}
+
+// Shares of the sums over rows: enough walkers over the rows to fill the chip
+// (4 workgroups to a compute unit), each at least one row.
+int64_t row_parts(int64_t rows, int64_t gd, int64_t groups) {
+    const int64_t walkers = is_wave(int(gd)) ? 4096 : 1024;
+    return std::max<int64_t>(1, std::min<int64_t>(rows, walkers / groups));
+}
+
+unsigned bwd_grid(int64_t units, int gd) { return unsigned(is_wave(gd) ? (units + 3) / 4 : units); }
+
+int check_norm(int64_t rows, int64_t d, int64_t groups, double eps) {
+    if (rows <= 0 || d <= 0 || groups <= 0 || rows > kMaxRows || d % groups != 0 || !sizes_ok({rows, d}))
+        return SS_ERR_SHAPE;
+    if (!(eps >= 0.0) || !std::isfinite(eps)) return SS_ERR_SHAPE;
+    if (d / groups > SS_MAX_NORM_CHANNELS || d >= (int64_t(1) << 31)) return SS_ERR_UNSUPPORTED;
+    return SS_OK;
+}
+
+bool stride_ok(int64_t rows, int64_t d, int64_t stride) { return stride >= d && stride <= kMaxElems / rows; }
+int64_t extent(int64_t rows, int64_t d, int64_t stride) { return (rows - 1) * stride + d; }
+
+template <typename T, typename TR>
+int run_residual(const NormParams& p, bool back, float* dweight, float* dscale, hipStream_t st) {
+    by_width(p.gd, [&](auto threads, auto vpt) {
+        constexpr int TH = decltype(threads)::value, V = decltype(vpt)::value;
+        const int block = block_threads(p.gd);
+        if (!back) {
+            const unsigned grid = fwd_grid(p.rows, p.gd);
+            ss::residual_norm_fwd<T, TR, TH, V><<<grid, block, 0, st>>>(p);
+        } else {
+            const unsigned grid = bwd_grid(p.parts, p.gd);
+            ss::residual_norm_bwd<T, TR, TH, V><<<grid, block, 0, st>>>(p);
+        }
+    });
+    if (back)
+        ss::norm_sum_parts<<<dim3(unsigned((p.d + 63) / 64), p.scale ? 2 : 1), 1024, 0, st>>>(p.part, dweight, dscale,
+                                                                                              p.parts, p.d);
+    return status(hipGetLastError());
+}
+
+int dispatch_residual(const NormParams& p, int dtype, int res_dtype, bool back, float* dweight,
+                      float* dscale, hipStream_t st) {
+    if (dtype == SS_F32) return run_residual<float, float>(p, back, dweight, dscale, st);
+    if (res_dtype == SS_F32) return run_residual<uint16_t, float>(p, back, dweight, dscale, st);
+    return run_residual<uint16_t, uint16_t>(p, back, dweight, dscale, st);
+}
+
+template <typename T>
+int run_gated(const NormParams& p, bool back, float* dweight, hipStream_t st) {
+    by_width(p.gd, [&](auto threads, auto vpt) {
+        constexpr int TH = decltype(threads)::value, V = decltype(vpt)::value;
+        const int block = block_threads(p.gd);
+        if (!back) {
+            const unsigned grid = fwd_grid(p.rows * p.groups, p.gd);
+            ss::gated_norm_fwd<T, TH, V><<<grid, block, 0, st>>>(p);
+        } else {
+            const unsigned grid = bwd_grid(int64_t(p.parts) * p.groups, p.gd);
+            ss::gated_norm_bwd<T, TH, V><<<grid, block, 0, st>>>(p);
+        }
+    });
+    if (back)
+        ss::norm_sum_parts<<<dim3(unsigned((p.d + 63) / 64), 1), 1024, 0, st>>>(p.part, dweight, nullptr, p.parts, p.d);
+    return status(hipGetLastError());
+}
+
+}  // namespace
+
+SS_EXPORT int ss_residual_norm_fwd(const void* x, const void* residual, const float* scale, const float* weight,
+                                   void* out, void* residual_out, int64_t rows, int64_t d, double eps, int dtype,
+                                   int res_dtype, int64_t x_stride, void* stream) {
+    if (!x || !weight || !out || !residual_out) return SS_ERR_NULL;
+    if (const int rc = check_norm(rows, d, 1, eps)) return rc;
+    if (!stride_ok(rows, d, x_stride)) return SS_ERR_SHAPE;
+    if (!dtype_ok(dtype) || (res_dtype != dtype && res_dtype != SS_F32)) return SS_ERR_DTYPE;
+    const size_t es = elem_size(dtype), er = elem_size(res_dtype);
+    if (!aligned(x, es) || !aligned(out, es) || !aligned(residual, er) || !aligned(residual_out, er) ||
+        !aligned(scale, 4) || !aligned(weight, 4))
+        return SS_ERR_ALIGN;
+    const Range rr = range_of(residual, rows * d, er), ro = range_of(residual_out, rows * d, er);
+    const Range ins[] = {range_of(x, extent(rows, d, x_stride), es), range_of(scale, d, 4), range_of(weight, d, 4),
+                         same(rr, ro) ? Range{0, 0} : rr};
+    const Range outs[] = {range_of(out, rows * d, es), ro};
+    if (!apart(ins, outs)) return SS_ERR_ALIAS;
+    NormParams p{};
+    p.x = x;
+    p.res = residual;
+    p.scale = scale;
+    p.w = weight;
+    p.out = out;
+    p.res_out = residual_out;
+    p.rows = rows;
+    p.d = d;
+    p.xs = x_stride;
+    p.gd = int(d);
+    p.groups = 1;
+    p.eps = float(eps);
+    return dispatch_residual(p, dtype, res_dtype, false, nullptr, nullptr, static_cast<hipStream_t>(stream));
+}
+
+SS_EXPORT size_t ss_residual_norm_bwd_workspace_bytes(int64_t rows, int64_t d) {
+    if (check_norm(rows, d, 1, 0.0) != SS_OK) return 0;
+    return round256(2 * size_t(row_parts(rows, d, 1)) * size_t(d) * sizeof(float));
+}
+
+SS_EXPORT int ss_residual_norm_bwd(const void* dout, const void* dresidual_out, const void* residual_out,
+                                   const void* x, const float* scale, const float* weight, void* dx, void* dresidual,
+                                   float* dweight, float* dscale, int64_t rows, int64_t d, double eps, int dtype,
+                                   int res_dtype, int64_t x_stride, void* workspace, size_t workspace_bytes,
+                                   void* stream) {
+    if (!dout || !residual_out || !weight || !dx || !dweight) return SS_ERR_NULL;
+    if ((scale != nullptr) != (dscale != nullptr) || (scale && !x)) return SS_ERR_NULL;
+    if (const int rc = check_norm(rows, d, 1, eps)) return rc;
+    if (scale && !stride_ok(rows, d, x_stride)) return SS_ERR_SHAPE;
+    if (!dtype_ok(dtype) || (res_dtype != dtype && res_dtype != SS_F32)) return SS_ERR_DTYPE;
+    const size_t es = elem_size(dtype), er = elem_size(res_dtype);
+    if (!scale) x = nullptr;
+    for (const void* p : {dout, x, static_cast<const void*>(dx)})
+        if (!aligned(p, es)) return SS_ERR_ALIGN;
+    for (const void* p : {dresidual_out, residual_out, static_cast<const void*>(dresidual)})
+        if (!aligned(p, er)) return SS_ERR_ALIGN;
+    for (const float* p : {scale, weight, static_cast<const float*>(dweight), static_cast<const float*>(dscale)})
+        if (!aligned(p, 4)) return SS_ERR_ALIGN;
+    const Range ins[] = {range_of(dout, rows * d, es), range_of(dresidual_out, rows * d, er),
+                         range_of(residual_out, rows * d, er), range_of(x, x ? extent(rows, d, x_stride) : 0, es),
+                         range_of(scale, d, 4), range_of(weight, d, 4)};
+    const Range outs[] = {range_of(dx, rows * d, es), range_of(dresidual, rows * d, er), range_of(dweight, d, 4),
+                          range_of(dscale, d, 4)};
+    if (!apart(ins, outs)) return SS_ERR_ALIAS;
+    const size_t need = ss_residual_norm_bwd_workspace_bytes(rows, d);
+    if (!workspace || workspace_bytes < need) return SS_ERR_WORKSPACE;
+    if (!aligned(workspace, 256)) return SS_ERR_ALIGN;
+    const Range rw[] = {range_of(workspace, int64_t(need), 1)};
+    if (!apart(ins, rw) || !apart(outs, rw)) return SS_ERR_ALIAS;
+    NormParams p{};
+    p.dout = dout;
+    p.dres_out = dresidual_out;
+    p.res = residual_out;
+    p.x = x;
+    p.scale = scale;
+    p.w = weight;
+    p.dx = dx;
+    p.dres = dresidual;
+    p.part = static_cast<float*>(workspace);
+    p.rows = rows;
+    p.d = d;
+    p.xs = x_stride;
+    p.gd = int(d);
+    p.groups = 1;
+    p.parts = int(row_parts(rows, d, 1));
+    p.eps = float(eps);
+    return dispatch_residual(p, dtype, res_dtype, true, dweight, dscale, static_cast<hipStream_t>(stream));
+}
+
+SS_EXPORT int ss_gated_norm_fwd(const void* y, const void* z, const float* weight, void* out, int64_t rows, int64_t d,
+                                int64_t groups, double eps, int norm_before_gate, int dtype, int64_t y_stride,
+                                int64_t z_stride, void* stream) {
+    if (!y || !z || !weight || !out) return SS_ERR_NULL;
+    if (const int rc = check_norm(rows, d, groups, eps)) return rc;
+    if (!stride_ok(rows, d, y_stride) || !stride_ok(rows, d, z_stride)) return SS_ERR_SHAPE;
+    if (!dtype_ok(dtype)) return SS_ERR_DTYPE;
+    const size_t es = elem_size(dtype);
+    if (!aligned(y, es) || !aligned(z, es) || !aligned(out, es) || !aligned(weight, 4)) return SS_ERR_ALIGN;
+    const Range ins[] = {range_of(y, extent(rows, d, y_stride), es), range_of(z, extent(rows, d, z_stride), es),
+                         range_of(weight, d, 4)};
+    const Range outs[] = {range_of(out, rows * d, es)};
+    if (!apart(ins, outs)) return SS_ERR_ALIAS;
+    NormParams p{};
+    p.x = y;
+    p.z = z;
+    p.w = weight;
+    p.out = out;
+    p.rows = rows;
+    p.d = d;
+    p.xs = y_stride;
+    p.zs = z_stride;
+    p.groups = int(groups);
+    p.gd = int(d / groups);
+    p.eps = float(eps);
+    p.before = norm_before_gate ? 1 : 0;
+    const hipStream_t st = static_cast<hipStream_t>(stream);
+    return dtype == SS_BF16 ? run_gated<uint16_t>(p, false, nullptr, st)
+                            : run_gated<float>(p, false, nullptr, st);
+}
+
+SS_EXPORT size_t ss_gated_norm_bwd_workspace_bytes(int64_t rows, int64_t d, int64_t groups) {
+    if (check_norm(rows, d, groups, 0.0) != SS_OK) return 0;
+    return round256(size_t(row_parts(rows, d / groups, groups)) * size_t(d) * sizeof(float));
+}
+
+SS_EXPORT int ss_gated_norm_bwd(const void* dout, const void* y, const void* z, const float* weight, void* dy,
+                                void* dz, float* dweight, int64_t rows, int64_t d, int64_t groups, double eps,
+                                int norm_before_gate, int dtype, int64_t y_stride, int64_t z_stride, void* workspace,
+                                size_t workspace_bytes, void* stream) {
+    if (!dout || !y || !z || !weight || !dy || !dz || !dweight) return SS_ERR_NULL;
+    if (const int rc = check_norm(rows, d, groups, eps)) return rc;
+    if (!stride_ok(rows, d, y_stride) || !stride_ok(rows, d, z_stride)) return SS_ERR_SHAPE;
+    if (!dtype_ok(dtype)) return SS_ERR_DTYPE;
+    const size_t es = elem_size(dtype);
+    for (const void* p : {dout, y, z, static_cast<const void*>(dy), static_cast<const void*>(dz)})
+        if (!aligned(p, es)) return SS_ERR_ALIGN;
+    if (!aligned(weight, 4) || !aligned(dweight, 4)) return SS_ERR_ALIGN;
+    const Range ins[] = {range_of(dout, rows * d, es), range_of(y, extent(rows, d, y_stride), es),
+                         range_of(z, extent(rows, d, z_stride), es), range_of(weight, d, 4)};
+    const Range outs[] = {range_of(dy, rows * d, es), range_of(dz, rows * d, es), range_of(dweight, d, 4)};
+    if (!apart(ins, outs)) return SS_ERR_ALIAS;
+    const size_t need = ss_gated_norm_bwd_workspace_bytes(rows, d, groups);
+    if (!workspace || workspace_bytes < need) return SS_ERR_WORKSPACE;
+    if (!aligned(workspace, 256)) return SS_ERR_ALIGN;
+    const Range rw[] = {range_of(workspace, int64_t(need), 1)};
+    if (!apart(ins, rw) || !apart(outs, rw)) return SS_ERR_ALIAS;
+    NormParams p{};
+    p.dout = dout;
+    p.x = y;
+    p.z = z;
+    p.w = weight;
+    p.dx = dy;
+    p.dz = dz;
+    p.part = static_cast<float*>(workspace);
+    p.rows = rows;
+    p.d = d;
+    p.xs = y_stride;
+    p.zs = z_stride;
+    p.groups = int(groups);
+    p.gd = int(d / groups);
+    p.parts = int(row_parts(rows, d / groups, groups));
+    p.eps = float(eps);
+    p.before = norm_before_gate ? 1 : 0;
+    const hipStream_t st = static_cast<hipStream_t>(stream);
+    return dtype == SS_BF16 ? run_gated<uint16_t>(p, true, dweight, st)
+                            : run_gated<float>(p, true, dweight, st);
+}
