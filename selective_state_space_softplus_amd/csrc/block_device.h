@@ -44,12 +44,18 @@ template <> struct Mat<uint16_t> {
         const u32x2 a = *reinterpret_cast<const u32x2*>(p), b = *reinterpret_cast<const u32x2*>(q);
         return __builtin_bit_cast(bf16x8, u32x4{a.x, a.y, b.x, b.y});
     }
-    // 8 elements `stride` apart.
-    static __device__ __forceinline__ Frag gather(const uint16_t* p, int stride) {
-        u32x4 v;
-#pragma unroll
-        for (int i = 0; i < 4; i++) v[i] = uint32_t(p[2 * i * stride]) | uint32_t(p[(2 * i + 1) * stride]) << 16;
-        return __builtin_bit_cast(bf16x8, v);
+    // The operand whose k are the LDS tile's rows k0 .. k0 + 31, for column c0 + lane % 16: two transposing reads.
+    // Each takes 4 rows of 16 columns from a group of 16 lanes, which name 4 columns of a row apiece, and gives
+    // every lane its column's 4 rows.
+    static __device__ __forceinline__ Frag columns(const uint16_t* tile, int ld, int k0, int c0) {
+        typedef short s16x4 __attribute__((ext_vector_type(4)));
+        const int lane = threadIdx.x & 63;
+        const uint16_t* const p = tile + (k0 + lane / 16 * 8 + lane % 16 / 4) * ld + c0 + lane % 4 * 4;
+        auto* const q = (__attribute__((address_space(3))) s16x4*)(p);
+        auto* const r = (__attribute__((address_space(3))) s16x4*)(p + 4 * ld);
+        const u32x2 a = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(q));
+        const u32x2 b = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(r));
+        return __builtin_bit_cast(bf16x8, u32x4{a.x, a.y, b.x, b.y});
     }
     // Rounded to nearest even: the operand's only rounding.
     static __device__ __forceinline__ Frag pack(f32x8 v) {
@@ -92,10 +98,12 @@ template <> struct Mat<float> {
         const f32x4 a = *reinterpret_cast<const f32x4*>(p), b = *reinterpret_cast<const f32x4*>(q);
         return Frag{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
     }
-    static __device__ __forceinline__ Frag gather(const float* p, int stride) {
+    static __device__ __forceinline__ Frag columns(const float* tile, int ld, int k0, int c0) {
+        const int lane = threadIdx.x & 63;
+        const float* const p = tile + (k0 + lane / 16 * 8) * ld + c0 + lane % 16;
         Frag v;
 #pragma unroll
-        for (int i = 0; i < 8; i++) v[i] = p[i * stride];
+        for (int i = 0; i < 8; i++) v[i] = p[i * ld];
         return v;
     }
     static __device__ __forceinline__ Frag pack(f32x8 v) { return v; }
@@ -115,6 +123,15 @@ __device__ __forceinline__ f32x4 mma_wide(typename Mat<T>::Frag a, const typenam
 #pragma unroll
     for (int i = Mat<T>::kWide - 1; i >= 0; i--) c = Mat<T>::mma(a, f[i], c);
     return c;
+}
+
+// Keeps the loads before it before the products after it: left to itself the
+// compiler puts each LDS load right before its product and waits for each
+// (~100 cycles, 72 of them per chunk in head_out).  Only with bf16, whose
+// fragments leave the registers to hold a stage's loads.
+template <typename T>
+__device__ __forceinline__ void issue_loads() {
+    if constexpr (sizeof(T) == 2) __builtin_amdgcn_sched_barrier(0);
 }
 
 // 4 values as 4 consecutive LDS elements (8- or 16-byte aligned).
@@ -159,35 +176,79 @@ struct Tile {
     static constexpr int kPerRow = COLS / kVec;
     static constexpr int kN = 64 * kPerRow / 256;
     static constexpr int kElems = 64 * kLd;
+    static constexpr int kRowStep = 256 / kPerRow;   // rows between a thread's vectors
     static_assert(64 * kPerRow % 256 == 0, "whole vectors per thread");
     u32x4 v[kN];
 
+    static __device__ __forceinline__ int row0() { return int(threadIdx.x) / kPerRow; }
+    static __device__ __forceinline__ int col0() { return int(threadIdx.x) % kPerRow * kVec; }
+
     __device__ __forceinline__ void load(const T* src, int64_t stride, int rows, int cols) {
+        const T* p = src + row0() * stride + col0();
+        if (rows == 64 && cols >= COLS) {
+#pragma unroll
+            for (int i = 0; i < kN; i++) v[i] = load16(p + i * kRowStep * stride);
+            return;
+        }
+        // Lanes outside read the first row and column instead and drop what they read.
+        const bool inside = col0() + kVec <= cols;
 #pragma unroll
         for (int i = 0; i < kN; i++) {
-            const int at = int(threadIdx.x) + 256 * i, row = at / kPerRow, col = at % kPerRow * kVec;
-            u32x4 w = {0, 0, 0, 0};
-            if (row < rows && col < cols) {
-                const T* p = src + row * stride + col;
-                if (col + kVec <= cols) {
-                    w = load16(p);
+            const bool ok = inside && row0() + i * kRowStep < rows;
+            v[i] = u32x4{0, 0, 0, 0};
+            if (cols >= kVec) {
+                const u32x4 w = load16(ok ? p + i * kRowStep * stride : src);
+                if (ok) v[i] = w;
+            }
+        }
+        if (cols < COLS && cols % kVec != 0 && col0() < cols && !inside) {   // the row's last, partial vector
+#pragma unroll
+            for (int i = 0; i < kN; i++)
+                if (row0() + i * kRowStep < rows)
+#pragma unroll
+                    for (int e = 0; e < kVec - 1; e++)
+                        if (col0() + e < cols) {
+                            const T x = p[i * kRowStep * stride + e];
+                            if constexpr (sizeof(T) == 2) v[i][e / 2] |= uint32_t(x) << (16 * (e % 2));
+                            else v[i][e] = __float_as_uint(x);
+                        }
+        }
+    }
+    // The tile's rows lo .. hi - 1 and columns inside, from LDS to memory.
+    static __device__ __forceinline__ void write(const T* lds, T* dst, int64_t stride, int lo, int hi, int cols) {
+        T* const p = dst + row0() * stride + col0();
+        const T* const q = lds + row0() * kLd + col0();
+        if (lo == 0 && hi == 64 && cols >= COLS) {
+#pragma unroll
+            for (int i = 0; i < kN; i++)
+                store16(p + i * kRowStep * stride, *reinterpret_cast<const u32x4*>(q + i * kRowStep * kLd));
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < kN; i++)
+            if (row0() + i * kRowStep >= lo && row0() + i * kRowStep < hi) {
+                if (col0() + kVec <= cols) {
+                    store16(p + i * kRowStep * stride, *reinterpret_cast<const u32x4*>(q + i * kRowStep * kLd));
                 } else {
 #pragma unroll
-                    for (int e = 0; e < kVec; e++)
-                        if (col + e < cols) {
-                            if constexpr (sizeof(T) == 2) w[e / 2] |= uint32_t(p[e]) << (16 * (e % 2));
-                            else w[e] = __float_as_uint(p[e]);
-                        }
+                    for (int e = 0; e < kVec - 1; e++)
+                        if (col0() + e < cols) p[i * kRowStep * stride + e] = q[i * kRowStep * kLd + e];
                 }
             }
-            v[i] = w;
-        }
     }
     __device__ __forceinline__ void store(T* lds) const {
 #pragma unroll
         for (int i = 0; i < kN; i++) {
-            const int at = int(threadIdx.x) + 256 * i, row = at / kPerRow, col = at % kPerRow * kVec;
-            *reinterpret_cast<u32x4*>(lds + row * kLd + col) = v[i];
+            *reinterpret_cast<u32x4*>(lds + (row0() + i * kRowStep) * kLd + col0()) = v[i];
+        }
+    }
+    // Rows lo .. hi - 1, and zeros in the others' place.
+    __device__ __forceinline__ void store_rows(T* lds, int lo, int hi) const {
+#pragma unroll
+        for (int i = 0; i < kN; i++) {
+            const int row = row0() + i * kRowStep;
+            const u32x4 zero = {0, 0, 0, 0};
+            *reinterpret_cast<u32x4*>(lds + row * kLd + col0()) = row >= lo && row < hi ? v[i] : zero;
         }
     }
     __device__ __forceinline__ bool non_finite() const {
@@ -197,6 +258,25 @@ struct Tile {
         return r;
     }
 };
+
+// Running sum over the 64 lanes, in 64 bits, by data-parallel moves: within rows
+// of 16 lanes first, then the rows' last sums on to the rows after.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp_or_zero(double v) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = uint32_t(__builtin_amdgcn_update_dpp(0, int(uint32_t(u)), CTRL, ROWS, 0xf, false));
+    const uint32_t hi = uint32_t(__builtin_amdgcn_update_dpp(0, int(uint32_t(u >> 32)), CTRL, ROWS, 0xf, false));
+    return __builtin_bit_cast(double, uint64_t(hi) << 32 | lo);
+}
+__device__ __forceinline__ double running_sum(double v) {
+    v += dpp_or_zero<0x111, 0xf>(v);   // row_shr:1
+    v += dpp_or_zero<0x112, 0xf>(v);
+    v += dpp_or_zero<0x114, 0xf>(v);
+    v += dpp_or_zero<0x118, 0xf>(v);
+    v += dpp_or_zero<0x142, 0xa>(v);   // row_bcast:15 into rows 1 and 3
+    v += dpp_or_zero<0x143, 0xc>(v);   // row_bcast:31 into rows 2 and 3
+    return v;
+}
 
 // Sum over the 16 lanes of a lane group, over the 4 groups, over the wave; in
 // every lane, in an order that does not vary.

@@ -70,17 +70,65 @@ __device__ __forceinline__ Gate make_gate(float delta, float bias, float a2, int
     Gate g;
     g.raw = delta + bias;
     g.step = valid ? (use_softplus ? softplus(g.raw) : g.raw) : 0.0f;
-    double c = valid ? fmaxf(g.step * a2, kLeastDecay) : 0.0f;
-    const int lane = threadIdx.x & 63;
-#pragma unroll
-    for (int m = 1; m < 64; m <<= 1) {
-        const double up = __shfl_up(c, m);
-        c += lane >= m ? up : 0.0;
-    }
+    const double c = running_sum(valid ? fmaxf(g.step * a2, kLeastDecay) : 0.0f);
     g.c.x = float(c);
     g.c.y = float(c - double(g.c.x));
     return g;
 }
+
+// A chunk's gates in LDS.
+struct GateLds {
+    f32x2 c[64];      // running sums
+    float step[64];
+    float in[64];     // exp(c_t): from the state before the chunk to step t
+    float out[64];    // exp(c_63 - c_t) s_t: from x_t to the state after the chunk
+    uint32_t flags[4];
+
+    // By one wave.
+    __device__ __forceinline__ void put(const Gate& g) {
+        const int lane = threadIdx.x & 63;
+        const f32x2 cq = {__builtin_bit_cast(float, __builtin_amdgcn_readlane(__float_as_int(g.c.x), 63)),
+                          __builtin_bit_cast(float, __builtin_amdgcn_readlane(__float_as_int(g.c.y), 63))};
+        c[lane] = g.c;
+        step[lane] = g.step;
+        in[lane] = exp2_hw(g.c.x);
+        out[lane] = exp2_hw(c_diff(cq, g.c)) * g.step;
+    }
+};
+
+// 8 floats at p (16-byte aligned).
+__device__ __forceinline__ f32x8 floats8(const float* p) { return Mat<float>::load(p); }
+__device__ __forceinline__ f32x4 floats4(const float* p) { return *reinterpret_cast<const f32x4*>(p); }
+
+// Each wave's word of `flags` says whether one of its lanes met a non-finite value.
+__device__ __forceinline__ void note_non_finite(uint32_t* flags, bool met) {
+    const bool any = __any(met);
+    if ((threadIdx.x & 63) == 0) flags[threadIdx.x >> 6] = any ? 1u : 0u;
+}
+__device__ __forceinline__ bool any_noted(const uint32_t* flags) {
+    const u32x4 f = *reinterpret_cast<const u32x4*>(flags);
+    return __builtin_amdgcn_readfirstlane(f[0] | f[1] | f[2] | f[3]) != 0;
+}
+
+// The steps of a chunk that are taken together: all of them, or, where x holds
+// an infinity or a NaN, one at a time.  The zeros that the products put in
+// place of later steps must not meet such a value: 0 times it is NaN.
+struct Steps {
+    bool single = false;
+    int lo = 0;   // the step, when single
+    __device__ __forceinline__ void begin() {
+        single = true;
+        lo = 0;
+    }
+    __device__ __forceinline__ bool has(int t, int rows) const { return single ? t == lo : t < rows; }
+    // On to the next step; whether the chunk is done.
+    __device__ __forceinline__ bool next(int rows) {
+        if (single && ++lo < rows) return false;
+        single = false;
+        lo = 0;
+        return true;
+    }
+};
 
 // Rows of the chunk that are inside the sequence.
 __device__ __forceinline__ int chunk_rows(const HeadParams& p, int chunk) {
@@ -97,15 +145,14 @@ enum class StateMode { Local, Chunks };
 //           at entry to every chunk goes to chunk_s or chunk_q, the last one to
 //           last / dh0 where a segment is the whole sequence.
 template <typename T, int NP, bool REV, StateMode MODE>
-__global__ __launch_bounds__(256) void head_states(HeadParams p) {
+__global__ __launch_bounds__(256, 2) void head_states(HeadParams p) {
     using M = Mat<T>;
     using TileK = Tile<T, NP>;
     using TileV = Tile<T, kHeadSlab>;
     extern __shared__ __align__(16) float smem[];
     T* const k_lds = reinterpret_cast<T*>(smem);
     T* const v_lds = k_lds + TileK::kElems;
-    f32x2* const c_lds = reinterpret_cast<f32x2*>(v_lds + TileV::kElems);   // c of the chunk
-    float* const s_lds = reinterpret_cast<float*>(c_lds + 64);                                        // steps
+    GateLds& gates = *reinterpret_cast<GateLds*>(v_lds + TileV::kElems);
 
     const uint32_t piece = piece_of(blockIdx.x, gridDim.x);
     const int hs = int(piece % uint32_t(p.H * p.slabs)), h = hs / p.slabs, slab = hs % p.slabs;
@@ -156,56 +203,54 @@ __global__ __launch_bounds__(256) void head_states(HeadParams p) {
     const int count = last - first + 1;
     fetch(REV ? last : first);
     float total = 0.0f;
-    for (int it = 0; it < count; it++) {
-        const int ck = REV ? last - it : first + it;
-        __syncthreads();
+    Steps steps;
+    for (int it = 0; it < count;) {
+        const int ck = REV ? last - it : first + it, rows = chunk_rows(p, ck);
+        barrier_lds();
         tk.store(k_lds);
-        tv.store(v_lds);
-        if (wave == 0) {
-            const Gate gt = make_gate(dl, bias, a2, p.softplus, lane < chunk_rows(p, ck));
-            c_lds[lane] = gt.c;
-            s_lds[lane] = gt.step;
+        if (!steps.single) tv.store(v_lds);
+        else tv.store_rows(v_lds, steps.lo, steps.lo + 1);
+        if (wave == 0) gates.put(make_gate(dl, bias, a2, p.softplus, steps.has(lane, rows)));
+        if (!REV) note_non_finite(gates.flags, tv.non_finite());
+        barrier_lds();
+        if (!REV && !steps.single && any_noted(gates.flags)) {
+            steps.begin();
+            continue;
         }
-        const bool odd = !REV && tv.non_finite();
-        const bool scalar = __syncthreads_or(odd) != 0;
-        if (it + 1 < count) fetch(REV ? ck - 1 : ck + 1);
-        if (MODE == StateMode::Chunks) {
+        const bool entry = steps.lo == 0, done = steps.next(rows);
+        if (done && it + 1 < count) fetch(REV ? ck - 1 : ck + 1);
+        if (MODE == StateMode::Chunks && entry) {
             float* const to = (REV ? p.chunk_q : p.chunk_s) + ((bh * p.slabs + slab) * p.chunks + ck) * (NP * 64);
 #pragma unroll
             for (int nt = 0; nt < NP / 16; nt++)
 #pragma unroll
                 for (int r = 0; r < 4; r++) to[(16 * nt + 4 * lg + r) * 64 + pc] = acc[nt][r];
         }
-        const f32x2 cq = c_lds[63];
-        const float decay = exp2_hw(cq.x);
-        total += cq.x;
+        typename M::Frag vf[2], kf[NP / 16];
+        f32x8 wv[2];
+#pragma unroll
+        for (int kk = 0; kk < 2; kk++) {
+            vf[kk] = M::columns(v_lds, TileV::kLd, 32 * kk, 16 * wave);
+            wv[kk] = floats8((REV ? gates.in : gates.out) + 32 * kk + 8 * lg);
+        }
+        const float cq = gates.c[63].x, decay = exp2_hw(cq);
+#pragma unroll
+        for (int nt = 0; nt < NP / 16; nt++) kf[nt] = M::columns(k_lds, TileK::kLd, 0, 16 * nt);
+        issue_loads<T>();
+        total += cq;
 #pragma unroll
         for (int nt = 0; nt < NP / 16; nt++) acc[nt] *= decay;
-        if (!scalar) {
 #pragma unroll
-            for (int kk = 0; kk < 2; kk++) {
-                const int j0 = 32 * kk + 8 * lg;
-                f32x8 wv = M::unpack(M::gather(v_lds + j0 * TileV::kLd + pc, TileV::kLd));
+        for (int kk = 0; kk < 2; kk++) {
+            typename M::Frag w[M::kWide];
+            M::split(M::unpack(vf[kk]) * wv[kk], w);
 #pragma unroll
-                for (int e = 0; e < 8; e++)
-                    wv[e] *= REV ? exp2_hw(c_lds[j0 + e].x) : exp2_hw(c_diff(cq, c_lds[j0 + e])) * s_lds[j0 + e];
-                typename M::Frag w[M::kWide];
-                M::split(wv, w);
-#pragma unroll
-                for (int nt = 0; nt < NP / 16; nt++)
-                    acc[nt] = mma_wide<T>(M::gather(k_lds + j0 * TileK::kLd + 16 * nt + lr, TileK::kLd), w, acc[nt]);
-            }
-        } else {
-            // An infinite or NaN x: multiply-adds give what the definition gives, where a sum of parts of it would not.
-            for (int j = 0; j < 64; j++) {
-                const float wx = exp2_hw(c_diff(cq, c_lds[j])) * s_lds[j] * widen(v_lds[j * TileV::kLd + pc]);
-#pragma unroll
-                for (int nt = 0; nt < NP / 16; nt++)
-#pragma unroll
-                    for (int r = 0; r < 4; r++)
-                        acc[nt][r] += wx * widen(k_lds[j * TileK::kLd + 16 * nt + 4 * lg + r]);
+            for (int nt = 0; nt < NP / 16; nt++) {
+                acc[nt] = mma_wide<T>(kf[nt], w, acc[nt]);
+                if (kk == 0) kf[nt] = M::columns(k_lds, TileK::kLd, 32, 16 * nt);
             }
         }
+        if (done) it++;
     }
     if (MODE == StateMode::Local) {
 #pragma unroll
@@ -259,7 +304,7 @@ __global__ __launch_bounds__(256) void head_carry(HeadParams p) {
 // rounded to bf16 in place as the second operand of the readout (its rows n
 // are the product's k: lane group g holds n = 4 g + 0..3 of two 16-row tiles).
 template <typename T, int NP>
-__global__ __launch_bounds__(256) void head_out(HeadParams p) {
+__global__ __launch_bounds__(256, 2) void head_out(HeadParams p) {
     using M = Mat<T>;
     using TileK = Tile<T, NP>;
     using TileV = Tile<T, kHeadSlab>;
@@ -268,8 +313,7 @@ __global__ __launch_bounds__(256) void head_out(HeadParams p) {
     T* const q_lds = b_lds + TileK::kElems;
     T* const x_lds = q_lds + TileK::kElems;
     T* const m_lds = x_lds + TileV::kElems;    // weighted scores [i][j]
-    f32x2* const c_lds = reinterpret_cast<f32x2*>(m_lds + TileV::kElems);
-    float* const s_lds = reinterpret_cast<float*>(c_lds + 64);
+    GateLds& gates = *reinterpret_cast<GateLds*>(m_lds + TileV::kElems);
 
     const uint32_t piece = piece_of(blockIdx.x, gridDim.x);
     const int hs = int(piece % uint32_t(p.H * p.slabs)), h = hs / p.slabs, slab = hs % p.slabs;
@@ -285,7 +329,7 @@ __global__ __launch_bounds__(256) void head_out(HeadParams p) {
     const T* const bb = static_cast<const T*>(p.B) + bi * p.Bb + int64_t(g) * p.N;
     const T* const cb = static_cast<const T*>(p.C) + bi * p.Cb + int64_t(g) * p.N;
     const T* const xb = static_cast<const T*>(p.x) + bi * p.xb + int64_t(h) * p.P + slab * kHeadSlab;
-    T* const yb = static_cast<T*>(p.y) + (bi * p.L * p.H + h) * p.P;
+    T* const yb = static_cast<T*>(p.y) + (bi * p.L * p.H + h) * p.P + slab * kHeadSlab;
     const int64_t yt = int64_t(p.H) * p.P;
     const int vcols = p.P - slab * kHeadSlab;
     const float a2 = a2_from_alog(p.A_log[h]), bias = p.bias ? p.bias[h] : 0.0f, skip = p.D[h];
@@ -314,111 +358,143 @@ __global__ __launch_bounds__(256) void head_out(HeadParams p) {
         tx.load(xb + t0 * p.xt, p.xt, rows, vcols);
         dl = gate_load<T>(p, bi, h, ck);
     };
+    // The outputs of a chunk replace its x in LDS (a wave's own columns), and leave from there in whole vectors: a
+    // thread's vectors of the tile are the ones it then overwrites.
+    auto write_y = [&](int ck, int lo, int hi) {
+        TileV::write(x_lds, yb + int64_t(ck) * kHeadChunk * yt, yt, lo, hi, vcols);
+    };
     fetch(first);
-    for (int ck = first; ck <= last; ck++) {
+    Steps steps;
+    int out_ck = -1, out_lo = 0, out_hi = 0;   // the outputs in x_lds
+    for (int ck = first; ck <= last;) {
         const int rows = chunk_rows(p, ck);
-        __syncthreads();
+        barrier_lds();
+        if (out_ck >= 0) write_y(out_ck, out_lo, out_hi);
+        out_ck = -1;
         tb.store(b_lds);
         tc.store(q_lds);
-        tx.store(x_lds);
-        if (wave == 0) {
-            const Gate gt = make_gate(dl, bias, a2, p.softplus, lane < rows);
-            c_lds[lane] = gt.c;
-            s_lds[lane] = gt.step;
+        if (!steps.single) tx.store(x_lds);
+        else tx.store_rows(x_lds, steps.lo, steps.lo + 1);
+        if (wave == 0) gates.put(make_gate(dl, bias, a2, p.softplus, steps.has(lane, rows)));
+        note_non_finite(gates.flags, tx.non_finite());
+        barrier_lds();
+        if (!steps.single && any_noted(gates.flags)) {
+            steps.begin();
+            continue;
         }
-        const bool scalar = __syncthreads_or(tx.non_finite()) != 0;
-        if (ck < last) fetch(ck + 1);
+        out_ck = ck;
+        out_lo = steps.lo;
+        out_hi = steps.single ? steps.lo + 1 : rows;
+        const bool done = steps.next(rows);
+        if (done && ck < last) fetch(ck + 1);
 
-        // Scores of rows i = 16 wave + lr, columns j = 16 jt + 4 lg + r, j <= i.
+        // Scores of rows i = 16 wave + lr, columns j = 16 jt + 4 lg + r; those of j > i are zeros.
+        const int i_row = 16 * wave + lr;
+        f32x4 sc[4];
         {
-            const int i = 16 * wave + lr;
-            const f32x2 ci = c_lds[i];
-            for (int jt = 0; jt <= (wave | 1); jt++) {
-                f32x4 s = {0, 0, 0, 0};
-                if (jt <= wave) {
+            typename M::Frag ci[NP / 32], bj[4][NP / 32];
 #pragma unroll
-                    for (int kk = 0; kk < NP / 32; kk++)
-                        s = M::mma(M::load(b_lds + (16 * jt + lr) * TileK::kLd + 32 * kk + 8 * lg),
-                                   M::load(q_lds + i * TileK::kLd + 32 * kk + 8 * lg), s);
+            for (int kk = 0; kk < NP / 32; kk++) ci[kk] = M::load(q_lds + i_row * TileK::kLd + 32 * kk + 8 * lg);
 #pragma unroll
-                    for (int r = 0; r < 4; r++) {
-                        const int j = 16 * jt + 4 * lg + r;
-                        s[r] = j <= i ? s[r] * (exp2_hw(c_diff(ci, c_lds[j])) * s_lds[j]) : 0.0f;
-                    }
-                }
-                store4(m_lds + i * TileV::kLd + 16 * jt + 4 * lg, s);
+            for (int jt = 0; jt < 4; jt++)
+#pragma unroll
+                for (int kk = 0; kk < NP / 32; kk++)
+                    bj[jt][kk] = M::load(b_lds + (16 * jt + lr) * TileK::kLd + 32 * kk + 8 * lg);
+            issue_loads<T>();
+#pragma unroll
+            for (int jt = 0; jt < 4; jt++) {
+                sc[jt] = f32x4{0, 0, 0, 0};
+#pragma unroll
+                for (int kk = 0; kk < NP / 32; kk++) sc[jt] = M::mma(bj[jt][kk], ci[kk], sc[jt]);
             }
         }
-        __syncthreads();
-
-        typename M::Frag xf[2];
+        // What the readout needs besides the scores.
+        typename M::Frag xf[2], cf[4][NP / 32], sf[NP / 32];
+        f32x4 ein[4];
 #pragma unroll
-        for (int kk = 0; kk < 2; kk++)
-            xf[kk] = M::gather(x_lds + (32 * kk + 8 * lg) * TileV::kLd + pc, TileV::kLd);
-        typename M::Frag sf[NP / 32];
+        for (int kk = 0; kk < 2; kk++) xf[kk] = M::columns(x_lds, TileV::kLd, 32 * kk, 16 * wave);
+#pragma unroll
+        for (int it = 0; it < 4; it++) {
+            const T* const cr = q_lds + (16 * it + lr) * TileK::kLd + 4 * lg;
+#pragma unroll
+            for (int kk = 0; kk < NP / 32; kk++) cf[it][kk] = M::load_2x4(cr + 32 * kk, cr + 32 * kk + 16);
+            ein[it] = floats4(gates.in + 16 * it + 4 * lg);
+        }
+        issue_loads<T>();
+        {
+            const f32x2 ci = gates.c[i_row];
+#pragma unroll
+            for (int jt = 0; jt < 4; jt++) {
+                const f32x4 sj = floats4(gates.step + 16 * jt + 4 * lg);
+#pragma unroll
+                for (int r = 0; r < 4; r++) {
+                    const int j = 16 * jt + 4 * lg + r;
+                    sc[jt][r] = j <= i_row ? sc[jt][r] * (exp2_hw(c_diff(ci, gates.c[j])) * sj[r]) : 0.0f;
+                }
+                store4(m_lds + i_row * TileV::kLd + 16 * jt + 4 * lg, sc[jt]);
+            }
+        }
 #pragma unroll
         for (int kk = 0; kk < NP / 32; kk++) {
             const f32x4 u = acc[2 * kk], v = acc[2 * kk + 1];
             sf[kk] = M::pack(f32x8{u[0], u[1], u[2], u[3], v[0], v[1], v[2], v[3]});
         }
+        barrier_lds();
+        typename M::Frag mf[4][2], kf[NP / 16];
+        f32x8 wv[2];
+        float xd[4][4];
 #pragma unroll
         for (int it = 0; it < 4; it++) {
-            f32x4 o = {0, 0, 0, 0};
-            const T* const cr = q_lds + (16 * it + lr) * TileK::kLd + 4 * lg;
 #pragma unroll
-            for (int kk = 0; kk < NP / 32; kk++)
-                o = M::mma(M::load_2x4(cr + 32 * kk, cr + 32 * kk + 16), sf[kk], o);
+            for (int kk = 0; kk <= it / 2; kk++)
+                mf[it][kk] = M::load(m_lds + (16 * it + lr) * TileV::kLd + 32 * kk + 8 * lg);
 #pragma unroll
-            for (int r = 0; r < 4; r++) o[r] *= exp2_hw(c_lds[16 * it + 4 * lg + r].x);
-            if (!scalar) {
-#pragma unroll
-                for (int kk = 0; kk <= it / 2; kk++)
-                    o = M::mma(M::load(m_lds + (16 * it + lr) * TileV::kLd + 32 * kk + 8 * lg), xf[kk], o);
-            } else {
-                // An infinite or NaN x must not meet the zeros of the scores of earlier rows.
-                for (int r = 0; r < 4; r++) {
-                    const int i = 16 * it + 4 * lg + r;
-                    for (int j = 0; j <= i; j++)
-                        o[r] += widen(m_lds[i * TileV::kLd + j]) * widen(x_lds[j * TileV::kLd + pc]);
-                }
-            }
-#pragma unroll
-            for (int r = 0; r < 4; r++) {
-                const int i = 16 * it + 4 * lg + r;
-                if (i < rows && pc < vcols)
-                    yb[(int64_t(ck) * kHeadChunk + i) * yt + pg] =
-                        narrow<T>(o[r] + skip * widen(x_lds[i * TileV::kLd + pc]));
-            }
+            for (int r = 0; r < 4; r++) xd[it][r] = widen(x_lds[(16 * it + 4 * lg + r) * TileV::kLd + pc]);
         }
-
-        const f32x2 cq = c_lds[63];
-        const float decay = exp2_hw(cq.x);
+        issue_loads<T>();
+        f32x4 out[4];
+#pragma unroll
+        for (int it = 0; it < 4; it++) out[it] = f32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int kk = 0; kk < NP / 32; kk++)
+#pragma unroll
+            for (int it = 0; it < 4; it++) out[it] = M::mma(cf[it][kk], sf[kk], out[it]);
+#pragma unroll
+        for (int kk = 0; kk < 2; kk++) wv[kk] = floats8(gates.out + 32 * kk + 8 * lg);
+#pragma unroll
+        for (int nt = 0; nt < NP / 16; nt++) kf[nt] = M::columns(b_lds, TileK::kLd, 0, 16 * nt);
+        issue_loads<T>();
+#pragma unroll
+        for (int it = 0; it < 4; it++) {
+            out[it] *= ein[it];
+#pragma unroll
+            for (int kk = 0; kk <= it / 2; kk++) out[it] = M::mma(mf[it][kk], xf[kk], out[it]);
+        }
+        const float decay = exp2_hw(gates.c[63].x);
 #pragma unroll
         for (int nt = 0; nt < NP / 16; nt++) acc[nt] *= decay;
-        if (!scalar) {
 #pragma unroll
-            for (int kk = 0; kk < 2; kk++) {
-                const int j0 = 32 * kk + 8 * lg;
-                f32x8 wv = M::unpack(xf[kk]);
+        for (int kk = 0; kk < 2; kk++) {
+            typename M::Frag w[M::kWide];
+            M::split(M::unpack(xf[kk]) * wv[kk], w);
 #pragma unroll
-                for (int e = 0; e < 8; e++) wv[e] *= exp2_hw(c_diff(cq, c_lds[j0 + e])) * s_lds[j0 + e];
-                typename M::Frag w[M::kWide];
-                M::split(wv, w);
-#pragma unroll
-                for (int nt = 0; nt < NP / 16; nt++)
-                    acc[nt] = mma_wide<T>(M::gather(b_lds + j0 * TileK::kLd + 16 * nt + lr, TileK::kLd), w, acc[nt]);
-            }
-        } else {
-            for (int j = 0; j < 64; j++) {
-                const float wx = exp2_hw(c_diff(cq, c_lds[j])) * s_lds[j] * widen(x_lds[j * TileV::kLd + pc]);
-#pragma unroll
-                for (int nt = 0; nt < NP / 16; nt++)
-#pragma unroll
-                    for (int r = 0; r < 4; r++)
-                        acc[nt][r] += wx * widen(b_lds[j * TileK::kLd + 16 * nt + 4 * lg + r]);
+            for (int nt = 0; nt < NP / 16; nt++) {
+                acc[nt] = mma_wide<T>(kf[nt], w, acc[nt]);
+                if (kk == 0) kf[nt] = M::columns(b_lds, TileK::kLd, 32, 16 * nt);
             }
         }
+#pragma unroll
+        for (int it = 0; it < 4; it++)
+#pragma unroll
+            for (int r = 0; r < 4; r++) out[it][r] += skip * xd[it][r];
+#pragma unroll
+        for (int it = 0; it < 4; it++)
+#pragma unroll
+            for (int r = 0; r < 4; r++) x_lds[(16 * it + 4 * lg + r) * TileV::kLd + pc] = narrow<T>(out[it][r]);
+        if (done) ck++;
     }
+    barrier_lds();
+    write_y(out_ck, out_lo, out_hi);
     if (p.nseg == 1 && p.last && pg < p.P)
 #pragma unroll
         for (int nt = 0; nt < NP / 16; nt++)
@@ -492,7 +568,7 @@ __global__ __launch_bounds__(256) void head_grad(HeadParams p) {
         tb.store(b_lds);
         tc.store(q_lds);
     }
-    __syncthreads();
+    barrier_lds();
     f32x4 cb[4];   // C_i . B_j, rows i = 16 wave + 4 lg + r, columns j = 16 jt + lr
 #pragma unroll
     for (int jt = 0; jt < 4; jt++) {
@@ -525,7 +601,7 @@ __global__ __launch_bounds__(256) void head_grad(HeadParams p) {
         float to_sum = 0.0f, from_sum = 0.0f, w_sum = 0.0f, dot_sum = 0.0f, d_sum = 0.0f;   // wave 0, lane t
         Gate gt{};
         for (int slab = 0; slab < p.slabs; slab++) {
-            __syncthreads();
+            barrier_lds();
             tx.store(x_lds);
             ty.store(dy_lds);
             if (wave == 0) {
@@ -533,7 +609,7 @@ __global__ __launch_bounds__(256) void head_grad(HeadParams p) {
                 c_lds[lane] = gt.c;
                 s_lds[lane] = gt.step;
             }
-            __syncthreads();
+            barrier_lds();
             if (slab + 1 < p.slabs) fetch(h, slab + 1);
             else if (h + 1 < h_last) fetch(h + 1, 0);
 
@@ -590,7 +666,7 @@ __global__ __launch_bounds__(256) void head_grad(HeadParams p) {
                 diag = sum_wave(diag);
                 if (lane == 0) dot_lds[4 + wave] = diag;
             }
-            __syncthreads();
+            barrier_lds();
 
             // dC, dB and the state terms.
             float dot = 0.0f;
@@ -615,8 +691,8 @@ __global__ __launch_bounds__(256) void head_grad(HeadParams p) {
                 for (int kk = 0; kk < 2; kk++) {
                     M::split(sv[kk], sf[kk]);
                     M::split(qv[kk], qf[kk]);
-                    bf[kk] = M::gather(b_lds + (32 * kk + 8 * lg) * TileK::kLd + n, TileK::kLd);
-                    cf[kk] = M::gather(q_lds + (32 * kk + 8 * lg) * TileK::kLd + n, TileK::kLd);
+                    bf[kk] = M::columns(b_lds, TileK::kLd, 32 * kk, n - lr);
+                    cf[kk] = M::columns(q_lds, TileK::kLd, 32 * kk, n - lr);
                 }
 #pragma unroll
                 for (int it = 0; it < 4; it++) {
@@ -637,7 +713,7 @@ __global__ __launch_bounds__(256) void head_grad(HeadParams p) {
                     }
 #pragma unroll
                     for (int kk = 0; kk <= it / 2; kk++)
-                        dc[it][nt] = M::mma(M::gather(r_lds + (32 * kk + 8 * lg) * TileV::kLd + 16 * it + lr, TileV::kLd),
+                        dc[it][nt] = M::mma(M::columns(r_lds, TileV::kLd, 32 * kk, 16 * it),
                                             bf[kk], dc[it][nt]);
 #pragma unroll
                     for (int kk = it / 2; kk < 2; kk++)
@@ -669,7 +745,7 @@ __global__ __launch_bounds__(256) void head_grad(HeadParams p) {
             }
 #pragma unroll
             for (int kk = 0; kk < 2; kk++)
-                df[kk] = M::gather(dy_lds + (32 * kk + 8 * lg) * TileV::kLd + pc, TileV::kLd);
+                df[kk] = M::columns(dy_lds, TileV::kLd, 32 * kk, 16 * wave);
             const bool inside = pc < p.P - slab * kHeadSlab;
             T* const dx = static_cast<T*>(p.dx) + (bi * p.L + t0) * dyt + int64_t(h) * p.P + slab * kHeadSlab + pc;
 #pragma unroll
@@ -690,7 +766,7 @@ __global__ __launch_bounds__(256) void head_grad(HeadParams p) {
                         dx[j * dyt] = narrow<T>(o[r] * s_lds[j] + skip * widen(dy_lds[j * TileV::kLd + pc]));
                 }
             }
-            __syncthreads();
+            barrier_lds();
             if (wave == 0) {
                 float yi = 0.0f, xi = 0.0f, ci = 0.0f;
 #pragma unroll
@@ -776,7 +852,7 @@ __global__ __launch_bounds__(256) void head_sum_chunks(HeadParams p) {
     for (int64_t i = threadIdx.x; i < count; i += 256) v += src[i * p.H];
     v = sum_wave(v);
     if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
-    __syncthreads();
+    barrier_lds();
     float* const out = k == 0 ? p.dA_log : k == 1 ? p.dbias : p.dD;
     if (threadIdx.x == 0 && out) out[h] = (part[0] + part[1]) + (part[2] + part[3]);
 }
@@ -824,11 +900,11 @@ __global__ __launch_bounds__(256) void head_step(float* state, const T* x, const
 // LDS bytes of the kernels above.
 template <typename T, int NP>
 constexpr size_t head_states_lds() {
-    return (Tile<T, NP>::kElems + Tile<T, kHeadSlab>::kElems) * sizeof(T) + 3 * 64 * sizeof(float);
+    return (Tile<T, NP>::kElems + Tile<T, kHeadSlab>::kElems) * sizeof(T) + sizeof(GateLds);
 }
 template <typename T, int NP>
 constexpr size_t head_out_lds() {
-    return (2 * Tile<T, NP>::kElems + 2 * Tile<T, kHeadSlab>::kElems) * sizeof(T) + 3 * 64 * sizeof(float);
+    return (2 * Tile<T, NP>::kElems + 2 * Tile<T, kHeadSlab>::kElems) * sizeof(T) + sizeof(GateLds);
 }
 
 template <typename T, int NP>
