@@ -61,11 +61,12 @@ size_t ss_head_scan_bwd_workspace_bytes(int64_t b, int64_t L, int64_t H, int64_t
  *   strides    : NULL for contiguous inputs, or 8 element counts: the batch and
  *                time strides of x, delta, B and C, in that order (a token's own
  *                elements are contiguous).  So x, B and C may be column ranges
- *                of one projection's rows.  Each at least 0 (SS_ERR_SHAPE).
+ *                of one projection's rows.  Each at least 0, the time strides
+ *                at most 2^24 (else SS_ERR_SHAPE).
  *   workspace  : ss_head_scan_fwd_workspace_bytes() bytes, 256-byte aligned; it
  *                needs no initialisation.
  * P <= SS_MAX_HEAD_DIM, N <= SS_MAX_HEAD_STATE (else SS_ERR_UNSUPPORTED),
- * L < 2^31 - 1024, b * H * ceil(P / 64) * ceil(L / 64) < 2^24 and every tensor
+ * L < 2^31 - 1024, H * P <= 2^24, b * H * ceil(P / 64) * ceil(L / 64) < 2^24 and every tensor
  * at most 2^46 elements (else SS_ERR_SHAPE).  A non-finite x, B, C or delta
  * reaches only the outputs at and after its time step that depend on it.
  * Results are the same bit for bit on every run.  Returns an ss_status.

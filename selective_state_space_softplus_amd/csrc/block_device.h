@@ -167,7 +167,9 @@ __device__ __forceinline__ bool any_non_finite(u32x4 v) {
 
 // A 64 x COLS tile of a strided source on its way to LDS: 256 threads hold
 // 16-byte vectors.  Rows at and beyond `rows` and columns at and beyond `cols`
-// are zero.  In LDS a row takes kLd elements, 16 bytes more than its data, so
+// become zero on the way into LDS; their loads, which are unconditional so
+// that nothing waits for them early, read the last row and vector inside
+// instead.  In LDS a row takes kLd elements, 16 bytes more than its data, so
 // that 16 rows' accesses at one column spread over the banks.
 template <typename T, int COLS>
 struct Tile {
@@ -183,35 +185,64 @@ struct Tile {
     static __device__ __forceinline__ int row0() { return int(threadIdx.x) / kPerRow; }
     static __device__ __forceinline__ int col0() { return int(threadIdx.x) % kPerRow * kVec; }
 
-    __device__ __forceinline__ void load(const T* src, int64_t stride, int rows, int cols) {
-        const T* p = src + row0() * stride + col0();
-        if (rows == 64 && cols >= COLS) {
+    // Rows `stride` elements apart (64 of them span less than 2^32 bytes), `before` elements of the same row before
+    // src.  Rows shorter than a vector are left to load_short(), called when the tile is stored.
+    static __device__ __forceinline__ bool is_short(int cols, int before) { return cols + before < kVec; }
+    __device__ __forceinline__ void load(const T* src, int64_t stride, int rows, int cols, int before = 0) {
+        const int last = cols - kVec, shift = min(0, last);   // the last vector's column, and where the first one starts
+        const char* const from = reinterpret_cast<const char*>(src + shift);
+        const uint32_t step = uint32_t(stride) * uint32_t(sizeof(T));
+        const uint32_t col = uint32_t(min(col0(), last) - shift) * uint32_t(sizeof(T));
+        uint32_t off[kN];   // bytes
+        if (rows == 64) {
 #pragma unroll
-            for (int i = 0; i < kN; i++) v[i] = load16(p + i * kRowStep * stride);
-            return;
+            for (int i = 0; i < kN; i++) off[i] = uint32_t(row0()) * step + col + uint32_t(i * kRowStep) * step;
+        } else {
+#pragma unroll
+            for (int i = 0; i < kN; i++) off[i] = uint32_t(min(row0() + i * kRowStep, rows - 1)) * step + col;
         }
-        // Lanes outside read the first row and column instead and drop what they read.
-        const bool inside = col0() + kVec <= cols;
+        if (!is_short(cols, before))
+#pragma unroll
+            for (int i = 0; i < kN; i++) v[i] = load16(reinterpret_cast<const T*>(from + off[i]));
+    }
+    __device__ __forceinline__ void load_short(const T* src, int64_t stride, int rows, int cols) {
 #pragma unroll
         for (int i = 0; i < kN; i++) {
-            const bool ok = inside && row0() + i * kRowStep < rows;
+            const T* const p = src + min(row0() + i * kRowStep, rows - 1) * stride;
             v[i] = u32x4{0, 0, 0, 0};
-            if (cols >= kVec) {
-                const u32x4 w = load16(ok ? p + i * kRowStep * stride : src);
-                if (ok) v[i] = w;
-            }
+#pragma unroll
+            for (int e = 0; e < kVec - 1; e++)
+                if (e < cols) {
+                    if constexpr (sizeof(T) == 2) v[i][e / 2] |= uint32_t(p[e]) << (16 * (e % 2));
+                    else v[i][e] = __float_as_uint(p[e]);
+                }
         }
-        if (cols < COLS && cols % kVec != 0 && col0() < cols && !inside) {   // the row's last, partial vector
+    }
+    // To LDS: rows lo .. hi - 1, and zeros in the others' place.
+    __device__ __forceinline__ void store(T* lds, int cols, int lo, int hi, int before = 0) const {
+        T* const q = lds + row0() * kLd + col0();
+        if (lo == 0 && hi == 64 && cols >= COLS) {
 #pragma unroll
-            for (int i = 0; i < kN; i++)
-                if (row0() + i * kRowStep < rows)
+            for (int i = 0; i < kN; i++) *reinterpret_cast<u32x4*>(q + i * kRowStep * kLd) = v[i];
+        } else {
+            // A partial vector was loaded from `late` elements before its place.
+            const int late = !is_short(cols, before) ? max(0, col0() + kVec - cols) : col0() < cols ? 0 : kVec;
+            const int bits = late * 8 * int(sizeof(T));
 #pragma unroll
-                    for (int e = 0; e < kVec - 1; e++)
-                        if (col0() + e < cols) {
-                            const T x = p[i * kRowStep * stride + e];
-                            if constexpr (sizeof(T) == 2) v[i][e / 2] |= uint32_t(x) << (16 * (e % 2));
-                            else v[i][e] = __float_as_uint(x);
-                        }
+            for (int i = 0; i < kN; i++) {
+                uint64_t a = uint64_t(v[i][1]) << 32 | v[i][0], b = uint64_t(v[i][3]) << 32 | v[i][2];
+                if (bits >= 64) {
+                    a = bits < 128 ? b >> (bits - 64) : 0;
+                    b = 0;
+                } else if (bits > 0) {
+                    a = a >> bits | b << (64 - bits);
+                    b >>= bits;
+                }
+                const int row = row0() + i * kRowStep;
+                const bool in = row >= lo && row < hi;
+                const u32x4 w = {uint32_t(a), uint32_t(a >> 32), uint32_t(b), uint32_t(b >> 32)}, zero = {0, 0, 0, 0};
+                *reinterpret_cast<u32x4*>(q + i * kRowStep * kLd) = in ? w : zero;
+            }
         }
     }
     // The tile's rows lo .. hi - 1 and columns inside, from LDS to memory.
@@ -235,21 +266,6 @@ struct Tile {
                         if (col0() + e < cols) p[i * kRowStep * stride + e] = q[i * kRowStep * kLd + e];
                 }
             }
-    }
-    __device__ __forceinline__ void store(T* lds) const {
-#pragma unroll
-        for (int i = 0; i < kN; i++) {
-            *reinterpret_cast<u32x4*>(lds + (row0() + i * kRowStep) * kLd + col0()) = v[i];
-        }
-    }
-    // Rows lo .. hi - 1, and zeros in the others' place.
-    __device__ __forceinline__ void store_rows(T* lds, int lo, int hi) const {
-#pragma unroll
-        for (int i = 0; i < kN; i++) {
-            const int row = row0() + i * kRowStep;
-            const u32x4 zero = {0, 0, 0, 0};
-            *reinterpret_cast<u32x4*>(lds + row * kLd + col0()) = row >= lo && row < hi ? v[i] : zero;
-        }
     }
     __device__ __forceinline__ bool non_finite() const {
         bool r = false;

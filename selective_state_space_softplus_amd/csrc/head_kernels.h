@@ -13,9 +13,9 @@
 // differences their digits (measured: 1.1e-5 relative after a decay of 2^-200,
 // 1e-6 with two).
 //
-// A workgroup of 4 waves holds the state of one head and a slab of 64 of its P
-// channels in accumulators, wave w channels 16 w .. 16 w + 15, and walks over
-// the chunks of its segment of the sequence.
+// A workgroup of 4 waves holds the states of one or two slabs of 64 of a head's
+// P channels in accumulators and walks over the chunks of its segment of the
+// sequence.
 #pragma once
 
 #include "block_device.h"
@@ -59,11 +59,11 @@ __device__ __forceinline__ float c_diff(f32x2 a, f32x2 b) { return (a.x - b.x) +
 // The least log2 of one step's decay: 2^-200 is 0 in fp32, and a finite sum has differences.
 constexpr float kLeastDecay = -200.0f;
 
+// delta of this lane's step, as it is in memory; past the sequence's end the last one's.
 template <typename T>
-__device__ __forceinline__ float gate_load(const HeadParams& p, int64_t bi, int h, int chunk) {
-    const int64_t t = int64_t(chunk) * kHeadChunk + (threadIdx.x & 63);
-    if (t >= p.L) return 0.0f;
-    return Elem<T>::load(static_cast<const T*>(p.delta), bi * p.deltab + t * p.deltat + h);
+__device__ __forceinline__ typename Raw<T>::type gate_load(const HeadParams& p, int64_t bi, int h, int chunk) {
+    const int64_t t = imin(int64_t(chunk) * kHeadChunk + (threadIdx.x & 63), p.L - 1);
+    return Raw<T>::load(static_cast<const T*>(p.delta), bi * p.deltab + t * p.deltat + h);
 }
 
 __device__ __forceinline__ Gate make_gate(float delta, float bias, float a2, int use_softplus, bool valid) {
@@ -120,7 +120,8 @@ struct Steps {
         single = true;
         lo = 0;
     }
-    __device__ __forceinline__ bool has(int t, int rows) const { return single ? t == lo : t < rows; }
+    __device__ __forceinline__ int end(int rows) const { return single ? lo + 1 : rows; }
+    __device__ __forceinline__ bool has(int t, int rows) const { return t >= lo && t < end(rows); }
     // On to the next step; whether the chunk is done.
     __device__ __forceinline__ bool next(int rows) {
         if (single && ++lo < rows) return false;
@@ -135,6 +136,168 @@ __device__ __forceinline__ int chunk_rows(const HeadParams& p, int chunk) {
     return int(imin(kHeadChunk, p.L - int64_t(chunk) * kHeadChunk));
 }
 
+// What a walking workgroup of 4 waves works on: JOBS (head, slab) pairs of one
+// group, which share its B and C tiles.  Each pair's 64 channels go to 4 / JOBS
+// waves, 16 JOBS channels to a wave, so that one fragment of B or C from LDS
+// meets JOBS column tiles.  A last, odd pair is done twice and written once.
+template <int JOBS>
+struct Walk {
+    static constexpr int kCols = 16 * JOBS;   // channels of a wave
+    int64_t bi;
+    int seg, g;
+    int h[JOBS], slab[JOBS];
+    bool alive[JOBS];
+    int job, my_h, my_slab;      // this wave's pair
+    bool my_alive;
+    int first, last;             // chunks
+    int p0;                      // this wave's first channel in the slab
+
+    __device__ __forceinline__ explicit Walk(const HeadParams& p) {
+        const int heads = p.H / p.G, jobs = heads * p.slabs, blocks = (jobs + JOBS - 1) / JOBS;
+        const uint32_t piece = piece_of(blockIdx.x, gridDim.x);
+        const int at = int(piece % uint32_t(p.G * blocks));
+        const uint32_t rest = piece / uint32_t(p.G * blocks);
+        g = at / blocks;
+        seg = int(rest % uint32_t(p.nseg));
+        bi = rest / uint32_t(p.nseg);
+#pragma unroll
+        for (int k = 0; k < JOBS; k++) {
+            const int q = at % blocks * JOBS + k, in = min(q, jobs - 1);
+            alive[k] = q < jobs;
+            h[k] = g * heads + in / p.slabs;
+            slab[k] = in % p.slabs;
+        }
+        first = seg * p.seg_chunks;
+        last = int(imin(int64_t(first) + p.seg_chunks, p.chunks)) - 1;
+        const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
+        job = wave * JOBS / 4;
+        p0 = wave % (4 / JOBS) * kCols;
+        my_h = h[0];
+        my_slab = slab[0];
+        my_alive = alive[0];
+#pragma unroll
+        for (int k = 1; k < JOBS; k++)
+            if (job == k) {
+                my_h = h[k];
+                my_slab = slab[k];
+                my_alive = alive[k];
+            }
+    }
+    // The head whose gates this wave (of the first JOBS) forms.
+    __device__ __forceinline__ int gate_head() const {
+        int v = h[0];
+#pragma unroll
+        for (int k = 1; k < JOBS; k++)
+            if (int(threadIdx.x) >> 6 == k) v = h[k];
+        return __builtin_amdgcn_readfirstlane(v);
+    }
+    // The padded state of this wave's job among `count` of them per (b, h, slab).
+    __device__ __forceinline__ int64_t state_at(const HeadParams& p, int np, int64_t count, int64_t i) const {
+        return (((bi * p.H + my_h) * p.slabs + my_slab) * count + i) * (np * 64);
+    }
+    // Element (n, p0 + 16 ct + lane % 16) of this wave's job in a (b, H, P, N) tensor; -1 outside.
+    __device__ __forceinline__ int64_t out_at(const HeadParams& p, int n, int ct) const {
+        const int pg = my_slab * kHeadSlab + p0 + 16 * ct + int(threadIdx.x & 15);
+        return n < p.N && pg < p.P ? ((bi * p.H + my_h) * p.P + pg) * p.N + n : -1;
+    }
+};
+
+// The wave's state from / to a padded (NP, 64) tile.
+template <int NP, int JOBS>
+__device__ __forceinline__ void state_load(f32x4 (&acc)[JOBS][NP / 16], const float* src, int p0) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int ct = 0; ct < JOBS; ct++)
+#pragma unroll
+        for (int nt = 0; nt < NP / 16; nt++)
+#pragma unroll
+            for (int r = 0; r < 4; r++)
+                acc[ct][nt][r] = src[(16 * nt + lane / 16 * 4 + r) * 64 + p0 + 16 * ct + lane % 16];
+}
+template <int NP, int JOBS>
+__device__ __forceinline__ void state_store(const f32x4 (&acc)[JOBS][NP / 16], float* dst, int p0) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int ct = 0; ct < JOBS; ct++)
+#pragma unroll
+        for (int nt = 0; nt < NP / 16; nt++)
+#pragma unroll
+            for (int r = 0; r < 4; r++)
+                dst[(16 * nt + lane / 16 * 4 + r) * 64 + p0 + 16 * ct + lane % 16] = acc[ct][nt][r];
+}
+// The same from / to a (b, H, P, N) tensor; NULL reads as zero.
+template <int NP, int JOBS>
+__device__ __forceinline__ void state_read(f32x4 (&acc)[JOBS][NP / 16], const HeadParams& p, const Walk<JOBS>& w,
+                                           const float* src) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int ct = 0; ct < JOBS; ct++)
+#pragma unroll
+        for (int nt = 0; nt < NP / 16; nt++)
+#pragma unroll
+            for (int r = 0; r < 4; r++) {
+                const int64_t at = w.out_at(p, 16 * nt + lane / 16 * 4 + r, ct);
+                acc[ct][nt][r] = src && at >= 0 ? src[at] : 0.0f;
+            }
+}
+template <int NP, int JOBS>
+__device__ __forceinline__ void state_write(const f32x4 (&acc)[JOBS][NP / 16], const HeadParams& p,
+                                            const Walk<JOBS>& w, float* dst) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int ct = 0; ct < JOBS; ct++)
+#pragma unroll
+        for (int nt = 0; nt < NP / 16; nt++)
+#pragma unroll
+            for (int r = 0; r < 4; r++) {
+                const int64_t at = w.out_at(p, 16 * nt + lane / 16 * 4 + r, ct);
+                if (at >= 0) dst[at] = acc[ct][nt][r];
+            }
+}
+
+// acc = decay * acc + K^T (w V): K a tile [step][n], V the wave's columns of a
+// tile [step][channel], w the steps' weights.
+template <typename T, int NP, int JOBS>
+__device__ __forceinline__ void state_update(f32x4 (&acc)[JOBS][NP / 16], float decay, const T* k_lds,
+                                             const typename Mat<T>::Frag (&vf)[JOBS][2], const float* weights) {
+    using M = Mat<T>;
+    constexpr int kLd = Tile<T, NP>::kLd;
+    const int lg = (threadIdx.x & 63) >> 4;
+    f32x8 wv[2];
+#pragma unroll
+    for (int kk = 0; kk < 2; kk++) wv[kk] = floats8(weights + 32 * kk + 8 * lg);
+    // Four fragments of K at a time, the next four on their way.
+    constexpr int kBatches = NP / 16 / 2;   // of both halves of the steps
+    typename M::Frag kf[2][4];
+    auto load_k = [&](int i) {
+#pragma unroll
+        for (int k = 0; k < 4; k++) {
+            const int at = 4 * i + k;
+            kf[i & 1][k] = M::columns(k_lds, kLd, at / (NP / 16) * 32, at % (NP / 16) * 16);
+        }
+    };
+    load_k(0);
+#pragma unroll
+    for (int ct = 0; ct < JOBS; ct++)
+#pragma unroll
+        for (int nt = 0; nt < NP / 16; nt++) acc[ct][nt] *= decay;
+    typename M::Frag w[JOBS][M::kWide];
+#pragma unroll
+    for (int i = 0; i < kBatches; i++) {
+        if (i + 1 < kBatches) load_k(i + 1);
+        issue_loads<T>();
+#pragma unroll
+        for (int k = 0; k < 4; k++) {
+            const int at = 4 * i + k, kk = at / (NP / 16), nt = at % (NP / 16);
+            if (nt == 0)
+#pragma unroll
+                for (int ct = 0; ct < JOBS; ct++) M::split(M::unpack(vf[ct][kk]) * wv[kk], w[ct]);
+#pragma unroll
+            for (int ct = 0; ct < JOBS; ct++) acc[ct][nt] = mma_wide<T>(kf[i & 1][k], w[ct], acc[ct][nt]);
+        }
+    }
+}
+
 enum class StateMode { Local, Chunks };
 
 // States over the sequence.
@@ -144,7 +307,7 @@ enum class StateMode { Local, Chunks };
 //   Chunks: from seg_state (several segments) or the given end state; the state
 //           at entry to every chunk goes to chunk_s or chunk_q, the last one to
 //           last / dh0 where a segment is the whole sequence.
-template <typename T, int NP, bool REV, StateMode MODE>
+template <typename T, int NP, int JOBS, bool REV, StateMode MODE>
 __global__ __launch_bounds__(256, 2) void head_states(HeadParams p) {
     using M = Mat<T>;
     using TileK = Tile<T, NP>;
@@ -152,122 +315,89 @@ __global__ __launch_bounds__(256, 2) void head_states(HeadParams p) {
     extern __shared__ __align__(16) float smem[];
     T* const k_lds = reinterpret_cast<T*>(smem);
     T* const v_lds = k_lds + TileK::kElems;
-    GateLds& gates = *reinterpret_cast<GateLds*>(v_lds + TileV::kElems);
+    GateLds* const gates = reinterpret_cast<GateLds*>(v_lds + JOBS * TileV::kElems);
 
-    const uint32_t piece = piece_of(blockIdx.x, gridDim.x);
-    const int hs = int(piece % uint32_t(p.H * p.slabs)), h = hs / p.slabs, slab = hs % p.slabs;
-    const uint32_t rest = piece / uint32_t(p.H * p.slabs);
-    const int seg = int(rest % uint32_t(p.nseg));
-    const int64_t bi = rest / uint32_t(p.nseg);
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, lr = lane & 15, lg = lane >> 4;
-    const int pc = 16 * wave + lr, pg = slab * kHeadSlab + pc;   // channel in the slab, in the head
-    const int64_t bh = bi * p.H + h;
-    const int g = h / (p.H / p.G);
-    const int first = seg * p.seg_chunks, last = int(imin(first + p.seg_chunks, p.chunks)) - 1;
-
-    const T* const kb = REV ? static_cast<const T*>(p.C) + bi * p.Cb + int64_t(g) * p.N
-                            : static_cast<const T*>(p.B) + bi * p.Bb + int64_t(g) * p.N;
+    const Walk<JOBS> w(p);
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int gate_head = w.gate_head();
+    const T* const kb = REV ? static_cast<const T*>(p.C) + w.bi * p.Cb + int64_t(w.g) * p.N
+                            : static_cast<const T*>(p.B) + w.bi * p.Bb + int64_t(w.g) * p.N;
     const int64_t kt = REV ? p.Ct : p.Bt;
-    const T* const vb = (REV ? static_cast<const T*>(p.dy) + bi * p.L * p.H * p.P
-                             : static_cast<const T*>(p.x) + bi * p.xb) + int64_t(h) * p.P + slab * kHeadSlab;
+    const T* const vb = REV ? static_cast<const T*>(p.dy) + w.bi * p.L * p.H * p.P
+                            : static_cast<const T*>(p.x) + w.bi * p.xb;
     const int64_t vt = REV ? int64_t(p.H) * p.P : p.xt;
-    const int vcols = p.P - slab * kHeadSlab;
-    const float a2 = a2_from_alog(p.A_log[h]), bias = p.bias ? p.bias[h] : 0.0f;
+    const float a2 = a2_from_alog(p.A_log[gate_head]), bias = p.bias ? p.bias[gate_head] : 0.0f;
 
-    f32x4 acc[NP / 16];
-    float* const seg_at = p.seg_state + ((bh * p.slabs + slab) * p.nseg + seg) * (NP * 64);
-    const float* const init = REV ? p.dlast : p.h0;
-#pragma unroll
-    for (int nt = 0; nt < NP / 16; nt++)
-#pragma unroll
-        for (int r = 0; r < 4; r++) {
-            const int n = 16 * nt + 4 * lg + r;
-            float v = 0.0f;
-            if (MODE == StateMode::Chunks) {
-                if (p.nseg > 1) v = seg_at[n * 64 + pc];
-                else if (init && n < p.N && pg < p.P) v = init[(bh * p.P + pg) * p.N + n];
-            }
-            acc[nt][r] = v;
-        }
+    f32x4 acc[JOBS][NP / 16];
+    float* const seg_at = p.seg_state + w.state_at(p, NP, p.nseg, w.seg);
+    if (MODE == StateMode::Chunks && p.nseg > 1) state_load<NP, JOBS>(acc, seg_at, w.p0);
+    else state_read<NP, JOBS>(acc, p, w, MODE == StateMode::Chunks ? (REV ? p.dlast : p.h0) : nullptr);
 
     TileK tk;
-    TileV tv;
-    float dl;
+    TileV tv[JOBS];
+    typename Raw<T>::type dl;
     auto fetch = [&](int ck) {
         const int64_t t0 = int64_t(ck) * kHeadChunk;
         const int rows = chunk_rows(p, ck);
         tk.load(kb + t0 * kt, kt, rows, p.N);
-        tv.load(vb + t0 * vt, vt, rows, vcols);
-        dl = gate_load<T>(p, bi, h, ck);
+#pragma unroll
+        for (int k = 0; k < JOBS; k++)
+            tv[k].load(vb + t0 * vt + int64_t(w.h[k]) * p.P + w.slab[k] * kHeadSlab, vt, rows,
+                       p.P - w.slab[k] * kHeadSlab, w.slab[k] * kHeadSlab);
+        dl = gate_load<T>(p, w.bi, gate_head, ck);
     };
-    const int count = last - first + 1;
-    fetch(REV ? last : first);
+    auto fetch_short = [&](int ck, int rows) {
+        const int64_t t0 = int64_t(ck) * kHeadChunk;
+        if (TileK::is_short(p.N, 0)) tk.load_short(kb + t0 * kt, kt, rows, p.N);
+#pragma unroll
+        for (int k = 0; k < JOBS; k++)
+            if (TileV::is_short(p.P, 0)) tv[k].load_short(vb + t0 * vt + int64_t(w.h[k]) * p.P, vt, rows, p.P);
+    };
+    const int count = w.last - w.first + 1;
+    fetch(REV ? w.last : w.first);
     float total = 0.0f;
     Steps steps;
     for (int it = 0; it < count;) {
-        const int ck = REV ? last - it : first + it, rows = chunk_rows(p, ck);
+        const int ck = REV ? w.last - it : w.first + it, rows = chunk_rows(p, ck);
         barrier_lds();
-        tk.store(k_lds);
-        if (!steps.single) tv.store(v_lds);
-        else tv.store_rows(v_lds, steps.lo, steps.lo + 1);
-        if (wave == 0) gates.put(make_gate(dl, bias, a2, p.softplus, steps.has(lane, rows)));
-        if (!REV) note_non_finite(gates.flags, tv.non_finite());
+        if (min(p.N, p.P) < TileK::kVec) fetch_short(ck, rows);
+        tk.store(k_lds, p.N, 0, rows);
+        bool met = false;
+#pragma unroll
+        for (int k = 0; k < JOBS; k++) {
+            tv[k].store(v_lds + k * TileV::kElems, p.P - w.slab[k] * kHeadSlab, steps.lo, steps.end(rows),
+                        w.slab[k] * kHeadSlab);
+            if (!REV) met |= tv[k].non_finite();
+        }
+        if (wave < JOBS) gates[wave].put(make_gate(Raw<T>::f(dl), bias, a2, p.softplus, steps.has(lane, rows)));
+        if (!REV) note_non_finite(gates[0].flags, met);
         barrier_lds();
-        if (!REV && !steps.single && any_noted(gates.flags)) {
+        if (!REV && !steps.single && any_noted(gates[0].flags)) {
             steps.begin();
             continue;
         }
         const bool entry = steps.lo == 0, done = steps.next(rows);
         if (done && it + 1 < count) fetch(REV ? ck - 1 : ck + 1);
-        if (MODE == StateMode::Chunks && entry) {
-            float* const to = (REV ? p.chunk_q : p.chunk_s) + ((bh * p.slabs + slab) * p.chunks + ck) * (NP * 64);
+        if (MODE == StateMode::Chunks && entry && w.my_alive)
+            state_store<NP, JOBS>(acc, (REV ? p.chunk_q : p.chunk_s) + w.state_at(p, NP, p.chunks, ck), w.p0);
+        typename M::Frag vf[JOBS][2];
 #pragma unroll
-            for (int nt = 0; nt < NP / 16; nt++)
+        for (int ct = 0; ct < JOBS; ct++)
 #pragma unroll
-                for (int r = 0; r < 4; r++) to[(16 * nt + 4 * lg + r) * 64 + pc] = acc[nt][r];
-        }
-        typename M::Frag vf[2], kf[NP / 16];
-        f32x8 wv[2];
-#pragma unroll
-        for (int kk = 0; kk < 2; kk++) {
-            vf[kk] = M::columns(v_lds, TileV::kLd, 32 * kk, 16 * wave);
-            wv[kk] = floats8((REV ? gates.in : gates.out) + 32 * kk + 8 * lg);
-        }
-        const float cq = gates.c[63].x, decay = exp2_hw(cq);
-#pragma unroll
-        for (int nt = 0; nt < NP / 16; nt++) kf[nt] = M::columns(k_lds, TileK::kLd, 0, 16 * nt);
-        issue_loads<T>();
+            for (int kk = 0; kk < 2; kk++)
+                vf[ct][kk] = M::columns(v_lds + w.job * TileV::kElems, TileV::kLd, 32 * kk, w.p0 + 16 * ct);
+        const GateLds& gt = gates[w.job];
+        const float cq = gt.c[63].x;
         total += cq;
-#pragma unroll
-        for (int nt = 0; nt < NP / 16; nt++) acc[nt] *= decay;
-#pragma unroll
-        for (int kk = 0; kk < 2; kk++) {
-            typename M::Frag w[M::kWide];
-            M::split(M::unpack(vf[kk]) * wv[kk], w);
-#pragma unroll
-            for (int nt = 0; nt < NP / 16; nt++) {
-                acc[nt] = mma_wide<T>(kf[nt], w, acc[nt]);
-                if (kk == 0) kf[nt] = M::columns(k_lds, TileK::kLd, 32, 16 * nt);
-            }
-        }
+        state_update<T, NP, JOBS>(acc, exp2_hw(cq), k_lds, vf, REV ? gt.in : gt.out);
         if (done) it++;
     }
+    if (!w.my_alive) return;
     if (MODE == StateMode::Local) {
-#pragma unroll
-        for (int nt = 0; nt < NP / 16; nt++)
-#pragma unroll
-            for (int r = 0; r < 4; r++) seg_at[(16 * nt + 4 * lg + r) * 64 + pc] = acc[nt][r];
-        if (slab == 0 && threadIdx.x == 0) p.seg_decay[bh * p.nseg + seg] = total;
-    } else if (p.nseg == 1) {
-        float* const out = REV ? p.dh0 : p.last;
-        if (out && pg < p.P)
-#pragma unroll
-            for (int nt = 0; nt < NP / 16; nt++)
-#pragma unroll
-                for (int r = 0; r < 4; r++) {
-                    const int n = 16 * nt + 4 * lg + r;
-                    if (n < p.N) out[(bh * p.P + pg) * p.N + n] = acc[nt][r];
-                }
+        state_store<NP, JOBS>(acc, seg_at, w.p0);
+        if (w.my_slab == 0 && lane == 0) p.seg_decay[(w.bi * p.H + w.my_h) * p.nseg + w.seg] = total;
+    } else if (p.nseg == 1 && (REV ? p.dh0 : p.last)) {
+        state_write<NP, JOBS>(acc, p, w, REV ? p.dh0 : p.last);
     }
 }
 
@@ -299,210 +429,223 @@ __global__ __launch_bounds__(256) void head_carry(HeadParams p) {
 
 // The outputs of a segment, and with one segment the last state.
 //
-// Per chunk: the scores B C^T, weighted, go through LDS as the first operand of
-// the product with x; the state, held as the accumulators of the update, is
-// rounded to bf16 in place as the second operand of the readout (its rows n
-// are the product's k: lane group g holds n = 4 g + 0..3 of two 16-row tiles).
-template <typename T, int NP>
+// Per chunk: the scores B C^T, formed once for the workgroup's pairs and
+// weighted for each, go through LDS as the first operand of the product with x;
+// the state, held as the accumulators of the update, is rounded to bf16 in
+// place as the second operand of the readout (its rows n are the product's k:
+// lane group g holds n = 4 g + 0..3 of two 16-row tiles).
+template <typename T, int NP, int JOBS>
 __global__ __launch_bounds__(256, 2) void head_out(HeadParams p) {
     using M = Mat<T>;
     using TileK = Tile<T, NP>;
     using TileV = Tile<T, kHeadSlab>;
+    constexpr int KN = NP / 32;
     extern __shared__ __align__(16) float smem[];
     T* const b_lds = reinterpret_cast<T*>(smem);
     T* const q_lds = b_lds + TileK::kElems;
     T* const x_lds = q_lds + TileK::kElems;
-    T* const m_lds = x_lds + TileV::kElems;    // weighted scores [i][j]
-    GateLds& gates = *reinterpret_cast<GateLds*>(m_lds + TileV::kElems);
+    T* const m_lds = x_lds + JOBS * TileV::kElems;    // weighted scores [i][j]
+    GateLds* const gates = reinterpret_cast<GateLds*>(m_lds + JOBS * TileV::kElems);
 
-    const uint32_t piece = piece_of(blockIdx.x, gridDim.x);
-    const int hs = int(piece % uint32_t(p.H * p.slabs)), h = hs / p.slabs, slab = hs % p.slabs;
-    const uint32_t rest = piece / uint32_t(p.H * p.slabs);
-    const int seg = int(rest % uint32_t(p.nseg));
-    const int64_t bi = rest / uint32_t(p.nseg);
+    const Walk<JOBS> w(p);
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, lr = lane & 15, lg = lane >> 4;
-    const int pc = 16 * wave + lr, pg = slab * kHeadSlab + pc;
-    const int64_t bh = bi * p.H + h;
-    const int g = h / (p.H / p.G);
-    const int first = seg * p.seg_chunks, last = int(imin(first + p.seg_chunks, p.chunks)) - 1;
-
-    const T* const bb = static_cast<const T*>(p.B) + bi * p.Bb + int64_t(g) * p.N;
-    const T* const cb = static_cast<const T*>(p.C) + bi * p.Cb + int64_t(g) * p.N;
-    const T* const xb = static_cast<const T*>(p.x) + bi * p.xb + int64_t(h) * p.P + slab * kHeadSlab;
-    T* const yb = static_cast<T*>(p.y) + (bi * p.L * p.H + h) * p.P + slab * kHeadSlab;
+    const int gate_head = w.gate_head();
+    const T* const bb = static_cast<const T*>(p.B) + w.bi * p.Bb + int64_t(w.g) * p.N;
+    const T* const cb = static_cast<const T*>(p.C) + w.bi * p.Cb + int64_t(w.g) * p.N;
+    const T* const xb = static_cast<const T*>(p.x) + w.bi * p.xb;
+    T* const yb = static_cast<T*>(p.y) + w.bi * p.L * p.H * p.P;
     const int64_t yt = int64_t(p.H) * p.P;
-    const int vcols = p.P - slab * kHeadSlab;
-    const float a2 = a2_from_alog(p.A_log[h]), bias = p.bias ? p.bias[h] : 0.0f, skip = p.D[h];
+    const float a2 = a2_from_alog(p.A_log[gate_head]), bias = p.bias ? p.bias[gate_head] : 0.0f;
+    const float skip = p.D[w.my_h];
 
-    f32x4 acc[NP / 16];
-    const float* const seg_at = p.seg_state + ((bh * p.slabs + slab) * p.nseg + seg) * (NP * 64);
-#pragma unroll
-    for (int nt = 0; nt < NP / 16; nt++)
-#pragma unroll
-        for (int r = 0; r < 4; r++) {
-            const int n = 16 * nt + 4 * lg + r;
-            float v = 0.0f;
-            if (p.nseg > 1) v = seg_at[n * 64 + pc];
-            else if (p.h0 && n < p.N && pg < p.P) v = p.h0[(bh * p.P + pg) * p.N + n];
-            acc[nt][r] = v;
-        }
+    f32x4 acc[JOBS][NP / 16];
+    if (p.nseg > 1) state_load<NP, JOBS>(acc, p.seg_state + w.state_at(p, NP, p.nseg, w.seg), w.p0);
+    else state_read<NP, JOBS>(acc, p, w, p.h0);
 
     TileK tb, tc;
-    TileV tx;
-    float dl;
+    TileV tx[JOBS];
+    typename Raw<T>::type dl;
     auto fetch = [&](int ck) {
         const int64_t t0 = int64_t(ck) * kHeadChunk;
         const int rows = chunk_rows(p, ck);
         tb.load(bb + t0 * p.Bt, p.Bt, rows, p.N);
         tc.load(cb + t0 * p.Ct, p.Ct, rows, p.N);
-        tx.load(xb + t0 * p.xt, p.xt, rows, vcols);
-        dl = gate_load<T>(p, bi, h, ck);
+#pragma unroll
+        for (int k = 0; k < JOBS; k++)
+            tx[k].load(xb + t0 * p.xt + int64_t(w.h[k]) * p.P + w.slab[k] * kHeadSlab, p.xt, rows,
+                       p.P - w.slab[k] * kHeadSlab, w.slab[k] * kHeadSlab);
+        dl = gate_load<T>(p, w.bi, gate_head, ck);
+    };
+    auto fetch_short = [&](int ck, int rows) {
+        const int64_t t0 = int64_t(ck) * kHeadChunk;
+        if (TileK::is_short(p.N, 0)) {
+            tb.load_short(bb + t0 * p.Bt, p.Bt, rows, p.N);
+            tc.load_short(cb + t0 * p.Ct, p.Ct, rows, p.N);
+        }
+#pragma unroll
+        for (int k = 0; k < JOBS; k++)
+            if (TileV::is_short(p.P, 0)) tx[k].load_short(xb + t0 * p.xt + int64_t(w.h[k]) * p.P, p.xt, rows, p.P);
     };
     // The outputs of a chunk replace its x in LDS (a wave's own columns), and leave from there in whole vectors: a
     // thread's vectors of the tile are the ones it then overwrites.
     auto write_y = [&](int ck, int lo, int hi) {
-        TileV::write(x_lds, yb + int64_t(ck) * kHeadChunk * yt, yt, lo, hi, vcols);
+#pragma unroll
+        for (int k = 0; k < JOBS; k++)
+            if (w.alive[k])
+                TileV::write(x_lds + k * TileV::kElems,
+                             yb + int64_t(ck) * kHeadChunk * yt + int64_t(w.h[k]) * p.P + w.slab[k] * kHeadSlab, yt, lo,
+                             hi, p.P - w.slab[k] * kHeadSlab);
     };
-    fetch(first);
+    T* const xj = x_lds + w.job * TileV::kElems;
+    const T* const mj = m_lds + w.job * TileV::kElems;
+    const GateLds& gt = gates[w.job];
+    fetch(w.first);
     Steps steps;
     int out_ck = -1, out_lo = 0, out_hi = 0;   // the outputs in x_lds
-    for (int ck = first; ck <= last;) {
+    for (int ck = w.first; ck <= w.last;) {
         const int rows = chunk_rows(p, ck);
         barrier_lds();
         if (out_ck >= 0) write_y(out_ck, out_lo, out_hi);
         out_ck = -1;
-        tb.store(b_lds);
-        tc.store(q_lds);
-        if (!steps.single) tx.store(x_lds);
-        else tx.store_rows(x_lds, steps.lo, steps.lo + 1);
-        if (wave == 0) gates.put(make_gate(dl, bias, a2, p.softplus, steps.has(lane, rows)));
-        note_non_finite(gates.flags, tx.non_finite());
+        if (min(p.N, p.P) < TileK::kVec) fetch_short(ck, rows);
+        tb.store(b_lds, p.N, 0, rows);
+        tc.store(q_lds, p.N, 0, rows);
+        bool met = false;
+#pragma unroll
+        for (int k = 0; k < JOBS; k++) {
+            tx[k].store(x_lds + k * TileV::kElems, p.P - w.slab[k] * kHeadSlab, steps.lo, steps.end(rows),
+                        w.slab[k] * kHeadSlab);
+            met |= tx[k].non_finite();
+        }
+        if (wave < JOBS) gates[wave].put(make_gate(Raw<T>::f(dl), bias, a2, p.softplus, steps.has(lane, rows)));
+        note_non_finite(gates[0].flags, met);
         barrier_lds();
-        if (!steps.single && any_noted(gates.flags)) {
+        if (!steps.single && any_noted(gates[0].flags)) {
             steps.begin();
             continue;
         }
         out_ck = ck;
         out_lo = steps.lo;
-        out_hi = steps.single ? steps.lo + 1 : rows;
+        out_hi = steps.end(rows);
         const bool done = steps.next(rows);
-        if (done && ck < last) fetch(ck + 1);
 
         // Scores of rows i = 16 wave + lr, columns j = 16 jt + 4 lg + r; those of j > i are zeros.
         const int i_row = 16 * wave + lr;
         f32x4 sc[4];
         {
-            typename M::Frag ci[NP / 32], bj[4][NP / 32];
+            typename M::Frag ci[2], bj[2][4];
+            auto load_bc = [&](int kk) {
+                ci[kk & 1] = M::load(q_lds + i_row * TileK::kLd + 32 * kk + 8 * lg);
 #pragma unroll
-            for (int kk = 0; kk < NP / 32; kk++) ci[kk] = M::load(q_lds + i_row * TileK::kLd + 32 * kk + 8 * lg);
+                for (int jt = 0; jt < 4; jt++)
+                    bj[kk & 1][jt] = M::load(b_lds + (16 * jt + lr) * TileK::kLd + 32 * kk + 8 * lg);
+            };
+            load_bc(0);
 #pragma unroll
-            for (int jt = 0; jt < 4; jt++)
+            for (int jt = 0; jt < 4; jt++) sc[jt] = f32x4{0, 0, 0, 0};
 #pragma unroll
-                for (int kk = 0; kk < NP / 32; kk++)
-                    bj[jt][kk] = M::load(b_lds + (16 * jt + lr) * TileK::kLd + 32 * kk + 8 * lg);
-            issue_loads<T>();
+            for (int kk = 0; kk < KN; kk++) {
+                if (kk + 1 < KN) load_bc(kk + 1);
+                issue_loads<T>();
 #pragma unroll
-            for (int jt = 0; jt < 4; jt++) {
-                sc[jt] = f32x4{0, 0, 0, 0};
-#pragma unroll
-                for (int kk = 0; kk < NP / 32; kk++) sc[jt] = M::mma(bj[jt][kk], ci[kk], sc[jt]);
+                for (int jt = 0; jt < 4; jt++) sc[jt] = M::mma(bj[kk & 1][jt], ci[kk & 1], sc[jt]);
             }
         }
         // What the readout needs besides the scores.
-        typename M::Frag xf[2], cf[4][NP / 32], sf[NP / 32];
-        f32x4 ein[4];
+        typename M::Frag xf[JOBS][2], cf[2][4];
+        auto load_c = [&](int kk) {
 #pragma unroll
-        for (int kk = 0; kk < 2; kk++) xf[kk] = M::columns(x_lds, TileV::kLd, 32 * kk, 16 * wave);
+            for (int it = 0; it < 4; it++) {
+                const T* const cr = q_lds + (16 * it + lr) * TileK::kLd + 4 * lg + 32 * kk;
+                cf[kk & 1][it] = M::load_2x4(cr, cr + 16);
+            }
+        };
 #pragma unroll
-        for (int it = 0; it < 4; it++) {
-            const T* const cr = q_lds + (16 * it + lr) * TileK::kLd + 4 * lg;
+        for (int ct = 0; ct < JOBS; ct++)
 #pragma unroll
-            for (int kk = 0; kk < NP / 32; kk++) cf[it][kk] = M::load_2x4(cr + 32 * kk, cr + 32 * kk + 16);
-            ein[it] = floats4(gates.in + 16 * it + 4 * lg);
-        }
+            for (int kk = 0; kk < 2; kk++) xf[ct][kk] = M::columns(xj, TileV::kLd, 32 * kk, w.p0 + 16 * ct);
+        load_c(0);
         issue_loads<T>();
-        {
-            const f32x2 ci = gates.c[i_row];
+#pragma unroll
+        for (int k = 0; k < JOBS; k++) {
+            const f32x2 ci = gates[k].c[i_row];
+            f32x4 c01[4], c23[4], sj[4];
 #pragma unroll
             for (int jt = 0; jt < 4; jt++) {
-                const f32x4 sj = floats4(gates.step + 16 * jt + 4 * lg);
+                const float* const cj = reinterpret_cast<const float*>(gates[k].c + 16 * jt + 4 * lg);
+                c01[jt] = floats4(cj);
+                c23[jt] = floats4(cj + 4);
+                sj[jt] = floats4(gates[k].step + 16 * jt + 4 * lg);
+            }
+            issue_loads<T>();
+#pragma unroll
+            for (int jt = 0; jt < 4; jt++) {
+                f32x4 m;
 #pragma unroll
                 for (int r = 0; r < 4; r++) {
-                    const int j = 16 * jt + 4 * lg + r;
-                    sc[jt][r] = j <= i_row ? sc[jt][r] * (exp2_hw(c_diff(ci, gates.c[j])) * sj[r]) : 0.0f;
+                    const f32x4 cc = r < 2 ? c01[jt] : c23[jt];
+                    const float e = exp2_hw(c_diff(ci, f32x2{cc[2 * (r & 1)], cc[2 * (r & 1) + 1]}));
+                    const float v = sc[jt][r] * (e * sj[jt][r]);
+                    m[r] = 16 * jt + 4 * lg + r <= i_row ? v : 0.0f;
                 }
-                store4(m_lds + i_row * TileV::kLd + 16 * jt + 4 * lg, sc[jt]);
+                store4(m_lds + k * TileV::kElems + i_row * TileV::kLd + 16 * jt + 4 * lg, m);
+            }
+        }
+        f32x4 out[JOBS][4];
+#pragma unroll
+        for (int ct = 0; ct < JOBS; ct++)
+#pragma unroll
+            for (int it = 0; it < 4; it++) out[ct][it] = f32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int kk = 0; kk < KN; kk++) {
+            if (kk + 1 < KN) load_c(kk + 1);
+            issue_loads<T>();
+#pragma unroll
+            for (int ct = 0; ct < JOBS; ct++) {
+                const f32x4 u = acc[ct][2 * kk], v = acc[ct][2 * kk + 1];
+                const typename M::Frag sf = M::pack(f32x8{u[0], u[1], u[2], u[3], v[0], v[1], v[2], v[3]});
+#pragma unroll
+                for (int it = 0; it < 4; it++) out[ct][it] = M::mma(cf[kk & 1][it], sf, out[ct][it]);
             }
         }
 #pragma unroll
-        for (int kk = 0; kk < NP / 32; kk++) {
-            const f32x4 u = acc[2 * kk], v = acc[2 * kk + 1];
-            sf[kk] = M::pack(f32x8{u[0], u[1], u[2], u[3], v[0], v[1], v[2], v[3]});
+        for (int it = 0; it < 4; it++) {
+            const f32x4 ein = floats4(gt.in + 16 * it + 4 * lg);
+#pragma unroll
+            for (int ct = 0; ct < JOBS; ct++) out[ct][it] *= ein;
         }
         barrier_lds();
-        typename M::Frag mf[4][2], kf[NP / 16];
-        f32x8 wv[2];
-        float xd[4][4];
+        if (done && ck < w.last) fetch(ck + 1);
+        typename M::Frag mf[4][2];
 #pragma unroll
-        for (int it = 0; it < 4; it++) {
+        for (int it = 0; it < 4; it++)
 #pragma unroll
             for (int kk = 0; kk <= it / 2; kk++)
-                mf[it][kk] = M::load(m_lds + (16 * it + lr) * TileV::kLd + 32 * kk + 8 * lg);
-#pragma unroll
-            for (int r = 0; r < 4; r++) xd[it][r] = widen(x_lds[(16 * it + 4 * lg + r) * TileV::kLd + pc]);
-        }
+                mf[it][kk] = M::load(mj + (16 * it + lr) * TileV::kLd + 32 * kk + 8 * lg);
         issue_loads<T>();
-        f32x4 out[4];
-#pragma unroll
-        for (int it = 0; it < 4; it++) out[it] = f32x4{0, 0, 0, 0};
-#pragma unroll
-        for (int kk = 0; kk < NP / 32; kk++)
-#pragma unroll
-            for (int it = 0; it < 4; it++) out[it] = M::mma(cf[it][kk], sf[kk], out[it]);
-#pragma unroll
-        for (int kk = 0; kk < 2; kk++) wv[kk] = floats8(gates.out + 32 * kk + 8 * lg);
-#pragma unroll
-        for (int nt = 0; nt < NP / 16; nt++) kf[nt] = M::columns(b_lds, TileK::kLd, 0, 16 * nt);
-        issue_loads<T>();
-#pragma unroll
-        for (int it = 0; it < 4; it++) {
-            out[it] *= ein[it];
-#pragma unroll
-            for (int kk = 0; kk <= it / 2; kk++) out[it] = M::mma(mf[it][kk], xf[kk], out[it]);
-        }
-        const float decay = exp2_hw(gates.c[63].x);
-#pragma unroll
-        for (int nt = 0; nt < NP / 16; nt++) acc[nt] *= decay;
-#pragma unroll
-        for (int kk = 0; kk < 2; kk++) {
-            typename M::Frag w[M::kWide];
-            M::split(M::unpack(xf[kk]) * wv[kk], w);
-#pragma unroll
-            for (int nt = 0; nt < NP / 16; nt++) {
-                acc[nt] = mma_wide<T>(kf[nt], w, acc[nt]);
-                if (kk == 0) kf[nt] = M::columns(b_lds, TileK::kLd, 32, 16 * nt);
-            }
-        }
 #pragma unroll
         for (int it = 0; it < 4; it++)
 #pragma unroll
-            for (int r = 0; r < 4; r++) out[it][r] += skip * xd[it][r];
+            for (int kk = 0; kk <= it / 2; kk++)
 #pragma unroll
-        for (int it = 0; it < 4; it++)
+                for (int ct = 0; ct < JOBS; ct++) out[ct][it] = M::mma(mf[it][kk], xf[ct][kk], out[ct][it]);
 #pragma unroll
-            for (int r = 0; r < 4; r++) x_lds[(16 * it + 4 * lg + r) * TileV::kLd + pc] = narrow<T>(out[it][r]);
+        for (int ct = 0; ct < JOBS; ct++) {
+            T* const at = xj + 4 * lg * TileV::kLd + w.p0 + 16 * ct + lr;
+            T xd[16];
+#pragma unroll
+            for (int k = 0; k < 16; k++) xd[k] = at[(k / 4 * 16 + k % 4) * TileV::kLd];
+            issue_loads<T>();
+#pragma unroll
+            for (int k = 0; k < 16; k++)
+                at[(k / 4 * 16 + k % 4) * TileV::kLd] = narrow<T>(out[ct][k / 4][k % 4] + skip * widen(xd[k]));
+        }
+        state_update<T, NP, JOBS>(acc, exp2_hw(gt.c[63].x), b_lds, xf, gt.out);
         if (done) ck++;
     }
     barrier_lds();
     write_y(out_ck, out_lo, out_hi);
-    if (p.nseg == 1 && p.last && pg < p.P)
-#pragma unroll
-        for (int nt = 0; nt < NP / 16; nt++)
-#pragma unroll
-            for (int r = 0; r < 4; r++) {
-                const int n = 16 * nt + 4 * lg + r;
-                if (n < p.N) p.last[(bh * p.P + pg) * p.N + n] = acc[nt][r];
-            }
+    if (p.nseg == 1 && p.last && w.my_alive) state_write<NP, JOBS>(acc, p, w, p.last);
 }
 
 // Gradients of one chunk for the heads of one head block of a group.
@@ -563,10 +706,16 @@ __global__ __launch_bounds__(256) void head_grad(HeadParams p) {
 
     {
         TileK tb, tc;
-        tb.load(static_cast<const T*>(p.B) + bi * p.Bb + t0 * p.Bt + int64_t(g) * p.N, p.Bt, rows, p.N);
-        tc.load(static_cast<const T*>(p.C) + bi * p.Cb + t0 * p.Ct + int64_t(g) * p.N, p.Ct, rows, p.N);
-        tb.store(b_lds);
-        tc.store(q_lds);
+        const T* const bb = static_cast<const T*>(p.B) + bi * p.Bb + t0 * p.Bt + int64_t(g) * p.N;
+        const T* const cb = static_cast<const T*>(p.C) + bi * p.Cb + t0 * p.Ct + int64_t(g) * p.N;
+        tb.load(bb, p.Bt, rows, p.N);
+        tc.load(cb, p.Ct, rows, p.N);
+        if (TileK::is_short(p.N, 0)) {
+            tb.load_short(bb, p.Bt, rows, p.N);
+            tc.load_short(cb, p.Ct, rows, p.N);
+        }
+        tb.store(b_lds, p.N, 0, rows);
+        tc.store(q_lds, p.N, 0, rows);
     }
     barrier_lds();
     f32x4 cb[4];   // C_i . B_j, rows i = 16 wave + 4 lg + r, columns j = 16 jt + lr
@@ -585,13 +734,15 @@ __global__ __launch_bounds__(256) void head_grad(HeadParams p) {
 #pragma unroll
         for (int nt = 0; nt < NW; nt++) db[it][nt] = dc[it][nt] = f32x4{0, 0, 0, 0};
 
+    const T* const xb = static_cast<const T*>(p.x) + bi * p.xb + t0 * p.xt;
+    const T* const dyb = static_cast<const T*>(p.dy) + (bi * p.L + t0) * dyt;
     TileV tx, ty;
-    float dl;
+    typename Raw<T>::type dl;
     auto fetch = [&](int h, int slab) {
         const int64_t col = int64_t(h) * p.P + slab * kHeadSlab;
         const int vcols = p.P - slab * kHeadSlab;
-        tx.load(static_cast<const T*>(p.x) + bi * p.xb + t0 * p.xt + col, p.xt, rows, vcols);
-        ty.load(static_cast<const T*>(p.dy) + (bi * p.L + t0) * dyt + col, dyt, rows, vcols);
+        tx.load(xb + col, p.xt, rows, vcols, slab * kHeadSlab);
+        ty.load(dyb + col, dyt, rows, vcols, slab * kHeadSlab);
         dl = gate_load<T>(p, bi, h, ck);
     };
     fetch(h_first, 0);
@@ -602,10 +753,14 @@ __global__ __launch_bounds__(256) void head_grad(HeadParams p) {
         Gate gt{};
         for (int slab = 0; slab < p.slabs; slab++) {
             barrier_lds();
-            tx.store(x_lds);
-            ty.store(dy_lds);
+            if (TileV::is_short(p.P, 0)) {
+                tx.load_short(xb + int64_t(h) * p.P, p.xt, rows, p.P);
+                ty.load_short(dyb + int64_t(h) * p.P, dyt, rows, p.P);
+            }
+            tx.store(x_lds, p.P - slab * kHeadSlab, 0, rows, slab * kHeadSlab);
+            ty.store(dy_lds, p.P - slab * kHeadSlab, 0, rows, slab * kHeadSlab);
             if (wave == 0) {
-                gt = make_gate(dl, bias, a2, p.softplus, lane < rows);
+                gt = make_gate(Raw<T>::f(dl), bias, a2, p.softplus, lane < rows);
                 c_lds[lane] = gt.c;
                 s_lds[lane] = gt.step;
             }
@@ -898,15 +1053,14 @@ __global__ __launch_bounds__(256) void head_step(float* state, const T* x, const
 }
 
 // LDS bytes of the kernels above.
-template <typename T, int NP>
+template <typename T, int NP, int JOBS>
 constexpr size_t head_states_lds() {
-    return (Tile<T, NP>::kElems + Tile<T, kHeadSlab>::kElems) * sizeof(T) + sizeof(GateLds);
+    return (Tile<T, NP>::kElems + JOBS * Tile<T, kHeadSlab>::kElems) * sizeof(T) + JOBS * sizeof(GateLds);
 }
-template <typename T, int NP>
+template <typename T, int NP, int JOBS>
 constexpr size_t head_out_lds() {
-    return (2 * Tile<T, NP>::kElems + 2 * Tile<T, kHeadSlab>::kElems) * sizeof(T) + sizeof(GateLds);
+    return (2 * Tile<T, NP>::kElems + 2 * JOBS * Tile<T, kHeadSlab>::kElems) * sizeof(T) + JOBS * sizeof(GateLds);
 }
-
 template <typename T, int NP>
 constexpr size_t head_grad_lds() {
     return (2 * Tile<T, NP>::kElems + 4 * Tile<T, kHeadSlab>::kElems) * sizeof(T) + (5 * 64 + 3 * 256 + 8) * sizeof(float);

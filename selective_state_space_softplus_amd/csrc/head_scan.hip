@@ -10,6 +10,8 @@ using ss::HeadParams;
 using ss::StateMode;
 
 constexpr int64_t kMaxLength = (int64_t(1) << 31) - 1024;
+// Largest time stride in elements: the 64 rows of a chunk then span less than 2^32 bytes.
+constexpr int64_t kMaxTimeStride = int64_t(1) << 24;
 constexpr int64_t kMaxPieces = int64_t(1) << 24;   // workgroups of 256 threads in one launch
 
 struct Shape {
@@ -21,7 +23,7 @@ struct Shape {
 int check_shape(const Shape& s, int dtype) {
     if (!sizes_ok({s.b, s.L, s.H, s.P}) || !sizes_ok({s.b, s.L, s.G, s.N}) || !sizes_ok({s.b, s.H, s.P, s.N}))
         return SS_ERR_SHAPE;
-    if (s.H % s.G != 0 || s.L > kMaxLength) return SS_ERR_SHAPE;
+    if (s.H % s.G != 0 || s.L > kMaxLength || s.H * s.P > kMaxTimeStride) return SS_ERR_SHAPE;
     if (!dtype_ok(dtype)) return SS_ERR_DTYPE;
     if (s.P > SS_MAX_HEAD_DIM || s.N > SS_MAX_HEAD_STATE) return SS_ERR_UNSUPPORTED;
     if (!sizes_ok({s.b, s.H, s.slabs(), s.chunks()}) || s.b * s.H * s.slabs() * s.chunks() >= kMaxPieces)
@@ -92,7 +94,7 @@ Strides strides_of(const Shape& s, const int64_t* given) {
 
 // Elements from a strided tensor's first to past its last; -1 where that is not below 2^46.
 int64_t extent(const Shape& s, int64_t sb, int64_t st, int64_t inner) {
-    if (sb < 0 || st < 0 || sb > kMaxElems / s.b || st > kMaxElems / s.L) return -1;
+    if (sb < 0 || st < 0 || sb > kMaxElems / s.b || st > kMaxTimeStride) return -1;
     const int64_t n = (s.b - 1) * sb + (s.L - 1) * st + inner;
     return n <= kMaxElems ? n : -1;
 }
@@ -130,29 +132,33 @@ HeadParams params_of(const Shape& s, const Strides& st, void* ws, bool grad) {
     return p;
 }
 
-template <typename T, int NP, bool REV>
-void carry_segments(const HeadParams& p, hipStream_t st) {
-    const unsigned walks = unsigned(p.b * p.H * p.slabs);
-    ss::head_states<T, NP, REV, StateMode::Local><<<walks * p.nseg, 256, ss::head_states_lds<T, NP>(), st>>>(p);
-    ss::head_carry<NP, REV><<<walks * (NP * 64 / 256), 256, 0, st>>>(p);
+// Workgroups of a walk over the sequence that take `jobs` (head, slab) pairs of a group each.
+unsigned walkers(const HeadParams& p, int jobs) {
+    return unsigned(p.b * p.nseg * p.G * ((p.H / p.G * p.slabs + jobs - 1) / jobs));
 }
 
-template <typename T, int NP>
+template <typename T, int NP, int JOBS, bool REV>
+void carry_segments(const HeadParams& p, hipStream_t st) {
+    ss::head_states<T, NP, JOBS, REV, StateMode::Local>
+        <<<walkers(p, JOBS), 256, ss::head_states_lds<T, NP, JOBS>(), st>>>(p);
+    ss::head_carry<NP, REV><<<unsigned(p.b * p.H * p.slabs) * (NP * 64 / 256), 256, 0, st>>>(p);
+}
+
+template <typename T, int NP, int JOBS>
 int run_fwd(const HeadParams& p, hipStream_t st) {
-    const unsigned walks = unsigned(p.b * p.H * p.slabs);
-    if (p.nseg > 1) carry_segments<T, NP, false>(p, st);
-    ss::head_out<T, NP><<<walks * p.nseg, 256, ss::head_out_lds<T, NP>(), st>>>(p);
+    if (p.nseg > 1) carry_segments<T, NP, JOBS, false>(p, st);
+    ss::head_out<T, NP, JOBS><<<walkers(p, JOBS), 256, ss::head_out_lds<T, NP, JOBS>(), st>>>(p);
     return status(hipGetLastError());
 }
 
-template <typename T, int NP>
+template <typename T, int NP, int JOBS>
 int run_bwd(HeadParams p, hipStream_t st) {
-    const unsigned walks = unsigned(p.b * p.H * p.slabs);
+    constexpr size_t lds = ss::head_states_lds<T, NP, JOBS>();
     p.last = nullptr;
-    if (p.nseg > 1) carry_segments<T, NP, false>(p, st);
-    ss::head_states<T, NP, false, StateMode::Chunks><<<walks * p.nseg, 256, ss::head_states_lds<T, NP>(), st>>>(p);
-    if (p.nseg > 1) carry_segments<T, NP, true>(p, st);
-    ss::head_states<T, NP, true, StateMode::Chunks><<<walks * p.nseg, 256, ss::head_states_lds<T, NP>(), st>>>(p);
+    if (p.nseg > 1) carry_segments<T, NP, JOBS, false>(p, st);
+    ss::head_states<T, NP, JOBS, false, StateMode::Chunks><<<walkers(p, JOBS), 256, lds, st>>>(p);
+    if (p.nseg > 1) carry_segments<T, NP, JOBS, true>(p, st);
+    ss::head_states<T, NP, JOBS, true, StateMode::Chunks><<<walkers(p, JOBS), 256, lds, st>>>(p);
     const unsigned grid = unsigned(p.b * p.chunks * p.G * p.blocks);
     ss::head_grad<T, NP><<<grid, 256, ss::head_grad_lds<T, NP>(), st>>>(p);
     if (p.blocks > 1) {
@@ -163,18 +169,39 @@ int run_bwd(HeadParams p, hipStream_t st) {
     return status(hipGetLastError());
 }
 
+// Pairs to a workgroup: two halve its LDS reads; fp32 fragments leave no
+// registers for it, and a group with one pair has no second.
+template <typename T>
+bool two_jobs(const HeadParams& p) {
+    return sizeof(T) == 2 && p.H / p.G * p.slabs > 1;
+}
+
+template <typename T, int NP>
+int fwd_jobs(const HeadParams& p, hipStream_t st) {
+    if constexpr (sizeof(T) == 2)
+        if (two_jobs<T>(p)) return run_fwd<T, NP, 2>(p, st);
+    return run_fwd<T, NP, 1>(p, st);
+}
+
+template <typename T, int NP>
+int bwd_jobs(const HeadParams& p, hipStream_t st) {
+    if constexpr (sizeof(T) == 2)
+        if (two_jobs<T>(p)) return run_bwd<T, NP, 2>(p, st);
+    return run_bwd<T, NP, 1>(p, st);
+}
+
 template <typename T>
 int dispatch_fwd(const HeadParams& p, hipStream_t st) {
     switch (padded_state(p.N, false)) {
-        case 32: return run_fwd<T, 32>(p, st);
-        case 64: return run_fwd<T, 64>(p, st);
-        default: return run_fwd<T, 128>(p, st);
+        case 32: return fwd_jobs<T, 32>(p, st);
+        case 64: return fwd_jobs<T, 64>(p, st);
+        default: return fwd_jobs<T, 128>(p, st);
     }
 }
 
 template <typename T>
 int dispatch_bwd(const HeadParams& p, hipStream_t st) {
-    return padded_state(p.N, true) == 64 ? run_bwd<T, 64>(p, st) : run_bwd<T, 128>(p, st);
+    return padded_state(p.N, true) == 64 ? bwd_jobs<T, 64>(p, st) : bwd_jobs<T, 128>(p, st);
 }
 
 template <typename T, bool VEC>
