@@ -165,21 +165,21 @@ __device__ __forceinline__ bool any_non_finite(u32x4 v) {
     return (r & top) != 0;
 }
 
-// A 64 x COLS tile of a strided source on its way to LDS: 256 threads hold
+// A 64 x COLS tile of a strided source on its way to LDS: THREADS threads hold
 // 16-byte vectors.  Rows at and beyond `rows` and columns at and beyond `cols`
 // become zero on the way into LDS; their loads, which are unconditional so
 // that nothing waits for them early, read the last row and vector inside
 // instead.  In LDS a row takes kLd elements, 16 bytes more than its data, so
 // that 16 rows' accesses at one column spread over the banks.
-template <typename T, int COLS>
+template <typename T, int COLS, int THREADS = 256>
 struct Tile {
     static constexpr int kVec = 16 / int(sizeof(T));
     static constexpr int kLd = COLS + kVec;
     static constexpr int kPerRow = COLS / kVec;
-    static constexpr int kN = 64 * kPerRow / 256;
+    static constexpr int kN = 64 * kPerRow / THREADS;
     static constexpr int kElems = 64 * kLd;
-    static constexpr int kRowStep = 256 / kPerRow;   // rows between a thread's vectors
-    static_assert(64 * kPerRow % 256 == 0, "whole vectors per thread");
+    static constexpr int kRowStep = THREADS / kPerRow;   // rows between a thread's vectors
+    static_assert(64 * kPerRow % THREADS == 0, "whole vectors per thread");
     u32x4 v[kN];
 
     static __device__ __forceinline__ int row0() { return int(threadIdx.x) / kPerRow; }
@@ -296,10 +296,15 @@ __device__ __forceinline__ double running_sum(double v) {
 
 // Sum over the 16 lanes of a lane group, over the 4 groups, over the wave; in
 // every lane, in an order that does not vary.
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xf, 0xf, false));
+}
 __device__ __forceinline__ float sum_lanes16(float v) {
-#pragma unroll
-    for (int m = 1; m < 16; m <<= 1) v += __shfl_xor(v, m);
-    return v;
+    v += dpp<0x128>(v);   // row_ror:8
+    v += dpp<0x124>(v);
+    v += dpp<0x122>(v);
+    return v + dpp<0x121>(v);
 }
 __device__ __forceinline__ float sum_groups4(float v) {
     v += __shfl_xor(v, 16);

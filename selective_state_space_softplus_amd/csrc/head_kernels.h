@@ -81,7 +81,8 @@ struct GateLds {
     f32x2 c[64];      // running sums
     float step[64];
     float in[64];     // exp(c_t): from the state before the chunk to step t
-    float out[64];    // exp(c_63 - c_t) s_t: from x_t to the state after the chunk
+    float rest[64];   // exp(c_63 - c_t): from step t to the state after the chunk
+    float out[64];    // the same times s_t: from x_t
     uint32_t flags[4];
 
     // By one wave.
@@ -92,7 +93,8 @@ struct GateLds {
         c[lane] = g.c;
         step[lane] = g.step;
         in[lane] = exp2_hw(g.c.x);
-        out[lane] = exp2_hw(c_diff(cq, g.c)) * g.step;
+        rest[lane] = exp2_hw(c_diff(cq, g.c));
+        out[lane] = rest[lane] * g.step;
     }
 };
 
@@ -665,29 +667,45 @@ __global__ __launch_bounds__(256, 2) void head_out(HeadParams p) {
 // R, the scores and the Q of dx, which only feed outputs of the inputs' type,
 // are rounded.
 //
-// Wave w owns rows 16 w.. of the score tiles, 16 NW columns n of dB and dC
-// (accumulated over heads in registers) and 16 columns of dx.
+// A workgroup of 8 waves takes one chunk and the heads of its block in turn.
+// The scores' 64 x 64 tile goes to the waves by two 16 x 16 pieces, dB and dC
+// (accumulated over heads in registers) by 16 columns n, dx by 16 columns and
+// 32 rows.  Two barriers a head: x, dy and the gates have two places in LDS,
+// and so have the shares of the sums, which wave 0 turns into ddelta while the
+// others are at the next head's scores.
+template <typename T>
+constexpr int kGradBuffers = sizeof(T) == 2 ? 2 : 1;   // fp32 tiles leave no LDS for a second place
+
+template <int NT>
+struct GradShares {
+    float row[2][64];       // sum_{j < i} W_ij of row i, by halves of j
+    float diag[64];         // W_ii / s_i
+    float col[16][64];      // sum_{i > j} W_ij / s_j of column j, by 4 rows i
+    float yin[NT][64];      // Y_i, by 16 columns n
+    float xin[NT][64];      // X_j / s_j
+    float dot[8], dsum[8];  // <Q, S> and the sum of G_ii, by wave
+};
+
 template <typename T, int NP>
-__global__ __launch_bounds__(256) void head_grad(HeadParams p) {
+struct GradLds {
+    static constexpr int kTileK = Tile<T, NP>::kElems, kTileV = Tile<T, kHeadSlab>::kElems;
+    T b[kTileK], c[kTileK];
+    T x[kGradBuffers<T>][kTileV], dy[kGradBuffers<T>][kTileV];
+    T m[kTileV], r[kTileV];                                // L_ij (C_i . B_j) and R_ij as [j][i]
+    T q[sizeof(T) == 2 ? NP * Tile<T, kHeadSlab>::kLd : 8];   // Q rounded, [n][channel]
+    GateLds gates[kGradBuffers<T>];
+    GradShares<NP / 16> shares[2];
+};
+
+template <typename T, int NP>
+__global__ __launch_bounds__(512, 2) void head_grad(HeadParams p) {
     using M = Mat<T>;
-    using TileK = Tile<T, NP>;
-    using TileV = Tile<T, kHeadSlab>;
-    constexpr int NW = NP / 64;
+    using TileK = Tile<T, NP, 512>;
+    using TileV = Tile<T, kHeadSlab, 512>;
+    constexpr int NT = NP / 16, ITW = NP / 32;   // tiles of n; row tiles of a wave's share of dB and dC
+    constexpr int kLdK = TileK::kLd, kLdV = TileV::kLd;
     extern __shared__ __align__(16) float smem[];
-    T* const b_lds = reinterpret_cast<T*>(smem);
-    T* const q_lds = b_lds + TileK::kElems;
-    T* const x_lds = q_lds + TileK::kElems;
-    T* const dy_lds = x_lds + TileV::kElems;
-    T* const m_lds = dy_lds + TileV::kElems;   // L_ij (C_i . B_j) as [j][i]
-    T* const r_lds = m_lds + TileV::kElems;    // R_ij as [j][i]
-    f32x2* const c_lds = reinterpret_cast<f32x2*>(r_lds + TileV::kElems);
-    float* const s_lds = reinterpret_cast<float*>(c_lds + 64);
-    float* const row_lds = s_lds + 64;         // sum_{j < i} W_ij
-    float* const diag_lds = row_lds + 64;      // W_ii / s_i
-    float* const col_lds = diag_lds + 64;      // [wave][j] sum_{i > j} W_ij / s_j
-    float* const yin_lds = col_lds + 256;      // [wave][i] share of Y_i
-    float* const xin_lds = yin_lds + 256;      // [wave][j] share of X_j / s_j
-    float* const dot_lds = xin_lds + 256;      // [wave] <Q, S>, [4 + wave] sum of G_ii
+    GradLds<T, NP>& lds = *reinterpret_cast<GradLds<T, NP>*>(smem);
 
     const uint32_t piece = piece_of(blockIdx.x, gridDim.x);
     const int hb = int(piece % uint32_t(p.blocks));
@@ -696,8 +714,12 @@ __global__ __launch_bounds__(256) void head_grad(HeadParams p) {
     rest /= uint32_t(p.G);
     const int ck = int(rest % uint32_t(p.chunks));
     const int64_t bi = rest / uint32_t(p.chunks);
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, lr = lane & 15, lg = lane >> 4;
-    const int pc = 16 * wave + lr;
+    const int lane = threadIdx.x & 63, lr = lane & 15, lg = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
+    const int si = wave >> 1, sj = 2 * (wave & 1);            // score tiles (si, sj) and (si, sj + 1)
+    const int nt = wave % NT, it0 = wave / NT * ITW;          // columns and row tiles of dB and dC
+    const int dp = 16 * (wave & 3) + lr, dj = 2 * (wave >> 2);   // column and row tiles of dx
+    const int n = 16 * nt + lr;
     const int64_t t0 = int64_t(ck) * kHeadChunk;
     const int rows = chunk_rows(p, ck), per_group = p.H / p.G;
     const int h_first = g * per_group + hb * p.per_block;
@@ -714,30 +736,15 @@ __global__ __launch_bounds__(256) void head_grad(HeadParams p) {
             tb.load_short(bb, p.Bt, rows, p.N);
             tc.load_short(cb, p.Ct, rows, p.N);
         }
-        tb.store(b_lds, p.N, 0, rows);
-        tc.store(q_lds, p.N, 0, rows);
+        tb.store(lds.b, p.N, 0, rows);
+        tc.store(lds.c, p.N, 0, rows);
     }
-    barrier_lds();
-    f32x4 cb[4];   // C_i . B_j, rows i = 16 wave + 4 lg + r, columns j = 16 jt + lr
-#pragma unroll
-    for (int jt = 0; jt < 4; jt++) {
-        cb[jt] = f32x4{0, 0, 0, 0};
-#pragma unroll
-        for (int kk = 0; kk < NP / 32; kk++)
-            cb[jt] = M::mma(M::load(q_lds + (16 * wave + lr) * TileK::kLd + 32 * kk + 8 * lg),
-                            M::load(b_lds + (16 * jt + lr) * TileK::kLd + 32 * kk + 8 * lg), cb[jt]);
-    }
-    const int n0 = 16 * NW * wave + lr;   // this lane's column n of the wave's first tile
-    f32x4 db[4][NW], dc[4][NW];
-#pragma unroll
-    for (int it = 0; it < 4; it++)
-#pragma unroll
-        for (int nt = 0; nt < NW; nt++) db[it][nt] = dc[it][nt] = f32x4{0, 0, 0, 0};
 
     const T* const xb = static_cast<const T*>(p.x) + bi * p.xb + t0 * p.xt;
     const T* const dyb = static_cast<const T*>(p.dy) + (bi * p.L + t0) * dyt;
     TileV tx, ty;
     typename Raw<T>::type dl;
+    f32x8 sv[2], qv[2];   // rows n of S and Q, channels 32 kk + 8 lg ..
     auto fetch = [&](int h, int slab) {
         const int64_t col = int64_t(h) * p.P + slab * kHeadSlab;
         const int vcols = p.P - slab * kHeadSlab;
@@ -745,241 +752,307 @@ __global__ __launch_bounds__(256) void head_grad(HeadParams p) {
         ty.load(dyb + col, dyt, rows, vcols, slab * kHeadSlab);
         dl = gate_load<T>(p, bi, h, ck);
     };
+    auto state_at = [&](int h, int slab) {
+        return (((bi * p.H + h) * p.slabs + slab) * p.chunks + ck) * (NP * 64);
+    };
+    auto fetch_states = [&](int h, int slab) {
+        const int64_t at = state_at(h, slab) + n * 64 + 8 * lg;
+#pragma unroll
+        for (int kk = 0; kk < 2; kk++) {
+            sv[kk] = floats8(p.chunk_s + at + 32 * kk);
+            qv[kk] = floats8(p.chunk_q + at + 32 * kk);
+        }
+    };
     fetch(h_first, 0);
-    for (int h = h_first; h < h_last; h++) {
-        const int64_t bh = bi * p.H + h;
-        const float a2 = a2_from_alog(p.A_log[h]), bias = p.bias ? p.bias[h] : 0.0f, skip = p.D[h];
-        float to_sum = 0.0f, from_sum = 0.0f, w_sum = 0.0f, dot_sum = 0.0f, d_sum = 0.0f;   // wave 0, lane t
-        Gate gt{};
-        for (int slab = 0; slab < p.slabs; slab++) {
-            barrier_lds();
-            if (TileV::is_short(p.P, 0)) {
-                tx.load_short(xb + int64_t(h) * p.P, p.xt, rows, p.P);
-                ty.load_short(dyb + int64_t(h) * p.P, dyt, rows, p.P);
-            }
-            tx.store(x_lds, p.P - slab * kHeadSlab, 0, rows, slab * kHeadSlab);
-            ty.store(dy_lds, p.P - slab * kHeadSlab, 0, rows, slab * kHeadSlab);
-            if (wave == 0) {
-                gt = make_gate(Raw<T>::f(dl), bias, a2, p.softplus, lane < rows);
-                c_lds[lane] = gt.c;
-                s_lds[lane] = gt.step;
-            }
-            barrier_lds();
-            if (slab + 1 < p.slabs) fetch(h, slab + 1);
-            else if (h + 1 < h_last) fetch(h + 1, 0);
+    fetch_states(h_first, 0);
+    barrier_lds();
 
-            const float* const s_at = p.chunk_s + ((bh * p.slabs + slab) * p.chunks + ck) * (NP * 64);
-            const float* const q_at = p.chunk_q + ((bh * p.slabs + slab) * p.chunks + ck) * (NP * 64);
-            const f32x2 cq = c_lds[63];
-
-            // Scores.
-            {
-                f32x4 row_sum = {0, 0, 0, 0};
-                float diag = 0.0f;
+    f32x4 cb[2];   // C_i . B_j, rows i = 16 si + 4 lg + r, columns j = 16 (sj + k) + lr
 #pragma unroll
-                for (int jt = 0; jt < 4; jt++) {
-                    const int j = 16 * jt + lr;
-                    float col = 0.0f;
-                    f32x4 gs = {0, 0, 0, 0}, ms = {0, 0, 0, 0}, rs = {0, 0, 0, 0};
-                    if (jt <= wave) {
+    for (int k = 0; k < 2; k++) {
+        cb[k] = f32x4{0, 0, 0, 0};
 #pragma unroll
-                        for (int kk = 0; kk < 2; kk++)
-                            gs = M::mma(M::load(dy_lds + (16 * wave + lr) * TileV::kLd + 32 * kk + 8 * lg),
-                                        M::load(x_lds + j * TileV::kLd + 32 * kk + 8 * lg), gs);
-                        const f32x2 cj = c_lds[j];
-                        const float sj = s_lds[j];
-#pragma unroll
-                        for (int r = 0; r < 4; r++) {
-                            const int i = 16 * wave + 4 * lg + r;
-                            if (j <= i) {
-                                const float w = exp2_hw(c_diff(c_lds[i], cj));
-                                ms[r] = w * cb[jt][r];
-                                rs[r] = w * gs[r] * sj;
-                                const float pr = ms[r] * gs[r];
-                                if (j < i) {
-                                    col += pr;
-                                    row_sum[r] += pr * sj;
-                                } else {
-                                    diag_lds[j] = pr;
-                                    diag += gs[r];
-                                }
-                            }
-                        }
-                    }
-                    if (jt <= (wave | 1)) {
-                        store4(m_lds + j * TileV::kLd + 16 * wave + 4 * lg, ms);
-                        store4(r_lds + j * TileV::kLd + 16 * wave + 4 * lg, rs);
-                    }
-                    col = sum_groups4(col);
-                    if (lg == 0) col_lds[64 * wave + j] = col;
-                }
-#pragma unroll
-                for (int r = 0; r < 4; r++) {
-                    const float v = sum_lanes16(row_sum[r]);
-                    if (lr == 0) row_lds[16 * wave + 4 * lg + r] = v;
-                }
-                diag = sum_wave(diag);
-                if (lane == 0) dot_lds[4 + wave] = diag;
-            }
-            barrier_lds();
-
-            // dC, dB and the state terms.
-            float dot = 0.0f;
-            float yin[4][4], xin[4][4];
-#pragma unroll
-            for (int it = 0; it < 4; it++)
-#pragma unroll
-                for (int r = 0; r < 4; r++) yin[it][r] = xin[it][r] = 0.0f;
-#pragma unroll
-            for (int nt = 0; nt < NW; nt++) {
-                const int n = n0 + 16 * nt;
-                f32x8 sv[2], qv[2];
-#pragma unroll
-                for (int kk = 0; kk < 2; kk++) {
-                    sv[kk] = Mat<float>::load(s_at + n * 64 + 32 * kk + 8 * lg);
-                    qv[kk] = Mat<float>::load(q_at + n * 64 + 32 * kk + 8 * lg);
-#pragma unroll
-                    for (int e = 0; e < 8; e++) dot += sv[kk][e] * qv[kk][e];
-                }
-                typename M::Frag sf[2][M::kWide], qf[2][M::kWide], bf[2], cf[2];
-#pragma unroll
-                for (int kk = 0; kk < 2; kk++) {
-                    M::split(sv[kk], sf[kk]);
-                    M::split(qv[kk], qf[kk]);
-                    bf[kk] = M::columns(b_lds, TileK::kLd, 32 * kk, n - lr);
-                    cf[kk] = M::columns(q_lds, TileK::kLd, 32 * kk, n - lr);
-                }
-#pragma unroll
-                for (int it = 0; it < 4; it++) {
-                    f32x4 u = {0, 0, 0, 0}, v = {0, 0, 0, 0};
-#pragma unroll
-                    for (int kk = 0; kk < 2; kk++) {
-                        u = mma_wide<T>(M::load(dy_lds + (16 * it + lr) * TileV::kLd + 32 * kk + 8 * lg), sf[kk], u);
-                        v = mma_wide<T>(M::load(x_lds + (16 * it + lr) * TileV::kLd + 32 * kk + 8 * lg), qf[kk], v);
-                    }
-#pragma unroll
-                    for (int r = 0; r < 4; r++) {
-                        const int i = 16 * it + 4 * lg + r;
-                        const float ui = u[r] * exp2_hw(c_lds[i].x), vi = v[r] * exp2_hw(c_diff(cq, c_lds[i]));
-                        yin[it][r] += ui * widen(q_lds[i * TileK::kLd + n]);
-                        xin[it][r] += vi * widen(b_lds[i * TileK::kLd + n]);
-                        dc[it][nt][r] += ui;
-                        db[it][nt][r] += vi * s_lds[i];
-                    }
-#pragma unroll
-                    for (int kk = 0; kk <= it / 2; kk++)
-                        dc[it][nt] = M::mma(M::columns(r_lds, TileV::kLd, 32 * kk, 16 * it),
-                                            bf[kk], dc[it][nt]);
-#pragma unroll
-                    for (int kk = it / 2; kk < 2; kk++)
-                        db[it][nt] = M::mma(M::load(r_lds + (16 * it + lr) * TileV::kLd + 32 * kk + 8 * lg), cf[kk],
-                                            db[it][nt]);
-                }
-            }
-#pragma unroll
-            for (int it = 0; it < 4; it++)
-#pragma unroll
-                for (int r = 0; r < 4; r++) {
-                    const float a = sum_lanes16(yin[it][r]), b = sum_lanes16(xin[it][r]);
-                    if (lr == 0) {
-                        yin_lds[64 * wave + 16 * it + 4 * lg + r] = a;
-                        xin_lds[64 * wave + 16 * it + 4 * lg + r] = b;
-                    }
-                }
-            dot = sum_wave(dot);
-            if (lane == 0) dot_lds[wave] = dot;
-
-            // dx.
-            typename M::Frag qb[NP / 32], df[2];
-#pragma unroll
-            for (int kk = 0; kk < NP / 32; kk++) {
-                f32x8 v;
-#pragma unroll
-                for (int e = 0; e < 8; e++) v[e] = q_at[(32 * kk + 8 * lg + e) * 64 + pc];
-                qb[kk] = M::pack(v);
-            }
-#pragma unroll
-            for (int kk = 0; kk < 2; kk++)
-                df[kk] = M::columns(dy_lds, TileV::kLd, 32 * kk, 16 * wave);
-            const bool inside = pc < p.P - slab * kHeadSlab;
-            T* const dx = static_cast<T*>(p.dx) + (bi * p.L + t0) * dyt + int64_t(h) * p.P + slab * kHeadSlab + pc;
-#pragma unroll
-            for (int jt = 0; jt < 4; jt++) {
-                f32x4 o = {0, 0, 0, 0};
-#pragma unroll
-                for (int kk = 0; kk < NP / 32; kk++)
-                    o = M::mma(M::load(b_lds + (16 * jt + lr) * TileK::kLd + 32 * kk + 8 * lg), qb[kk], o);
-#pragma unroll
-                for (int r = 0; r < 4; r++) o[r] *= exp2_hw(c_diff(cq, c_lds[16 * jt + 4 * lg + r]));
-#pragma unroll
-                for (int kk = jt / 2; kk < 2; kk++)
-                    o = M::mma(M::load(m_lds + (16 * jt + lr) * TileV::kLd + 32 * kk + 8 * lg), df[kk], o);
-#pragma unroll
-                for (int r = 0; r < 4; r++) {
-                    const int j = 16 * jt + 4 * lg + r;
-                    if (j < rows && inside)
-                        dx[j * dyt] = narrow<T>(o[r] * s_lds[j] + skip * widen(dy_lds[j * TileV::kLd + pc]));
-                }
-            }
-            barrier_lds();
-            if (wave == 0) {
-                float yi = 0.0f, xi = 0.0f, ci = 0.0f;
-#pragma unroll
-                for (int w = 0; w < 4; w++) {
-                    yi += yin_lds[64 * w + lane];
-                    xi += xin_lds[64 * w + lane];
-                    ci += col_lds[64 * w + lane];
-                    dot_sum += dot_lds[w];
-                    d_sum += dot_lds[4 + w];
-                }
-                to_sum += row_lds[lane] - gt.step * ci + yi;
-                from_sum += gt.step * xi;
-                w_sum += diag_lds[lane] + ci + xi;
-            }
-        }
-        if (wave == 0) {
-            float to = to_sum, from = from_sum;   // sums over steps >= t, and < t
-#pragma unroll
-            for (int m = 1; m < 64; m <<= 1) {
-                const float down = __shfl_down(to, m), up = __shfl_up(from, m);
-                to += lane + m < 64 ? down : 0.0f;
-                from += lane >= m ? up : 0.0f;
-            }
-            from = __shfl_up(from, 1);
-            const float dlog = to + (lane > 0 ? from : 0.0f) + exp2_hw(c_lds[63].x) * dot_sum;
-            const float a = a2 * kLn2;
-            float dstep = a * dlog + w_sum;   // w_sum lacks the step: it is what it is the gradient of
-            if (p.softplus) dstep *= rcp_hw(1.0f + exp2_hw(-gt.raw * kLog2e));
-            if (lane < rows)
-                static_cast<T*>(p.ddelta)[(bi * p.L + t0 + lane) * p.H + h] = narrow<T>(dstep);
-            const float da = sum_wave(lane < rows ? dlog * gt.step * a : 0.0f);
-            const float dbias = sum_wave(lane < rows ? dstep : 0.0f);
-            if (lane == 0) {
-                const int64_t at = (bi * p.chunks + ck) * p.H + h, one = p.b * p.chunks * p.H;
-                p.partial[at] = da;
-                p.partial[one + at] = dbias;
-                p.partial[2 * one + at] = d_sum;
-            }
-        }
+        for (int kk = 0; kk < NP / 32; kk++)
+            cb[k] = M::mma(M::load(lds.c + (16 * si + lr) * kLdK + 32 * kk + 8 * lg),
+                           M::load(lds.b + (16 * (sj + k) + lr) * kLdK + 32 * kk + 8 * lg), cb[k]);
     }
+    typename M::Frag bf[2], cf[2];   // B and C as operands, steps by column n
 #pragma unroll
-    for (int it = 0; it < 4; it++)
+    for (int kk = 0; kk < 2; kk++) {
+        bf[kk] = M::columns(lds.b, kLdK, 32 * kk, 16 * nt);
+        cf[kk] = M::columns(lds.c, kLdK, 32 * kk, 16 * nt);
+    }
+    f32x4 db[ITW], dc[ITW];
 #pragma unroll
-        for (int nt = 0; nt < NW; nt++)
+    for (int k = 0; k < ITW; k++) db[k] = dc[k] = f32x4{0, 0, 0, 0};
+
+    // Sums over the slabs of a head (wave 0, lane t), and what its ddelta takes.
+    float to_sum = 0.0f, from_sum = 0.0f, w_sum = 0.0f, dot_sum = 0.0f, d_sum = 0.0f;
+    Gate gt{}, old{};
+    float a2 = 0.0f, bias = 0.0f, old_a2 = 0.0f;
+    auto finish = [&](const GradShares<NT>& sh, int h, bool done) {
+        float yi = 0.0f, xi = 0.0f, ci = 0.0f;
+#pragma unroll
+        for (int k = 0; k < NT; k++) {
+            yi += sh.yin[k][lane];
+            xi += sh.xin[k][lane];
+        }
+#pragma unroll
+        for (int k = 0; k < 16; k++) ci += sh.col[k][lane];
+#pragma unroll
+        for (int k = 0; k < 8; k++) {
+            if (k < NT) dot_sum += sh.dot[k];
+            d_sum += sh.dsum[k];
+        }
+        to_sum += sh.row[0][lane] + sh.row[1][lane] - old.step * ci + yi;
+        from_sum += old.step * xi;
+        w_sum += sh.diag[lane] + ci + xi;
+        if (!done) return;
+        float to = to_sum, from = from_sum;   // sums over steps >= t, and < t
+#pragma unroll
+        for (int m = 1; m < 64; m <<= 1) {
+            const float down = __shfl_down(to, m), up = __shfl_up(from, m);
+            to += lane + m < 64 ? down : 0.0f;
+            from += lane >= m ? up : 0.0f;
+        }
+        from = __shfl_up(from, 1);
+        const float decay = exp2_hw(__int_as_float(__builtin_amdgcn_readlane(__float_as_int(old.c.x), 63)));
+        const float dlog = to + (lane > 0 ? from : 0.0f) + decay * dot_sum;
+        const float a = old_a2 * kLn2;
+        float dstep = a * dlog + w_sum;   // w_sum lacks the step: it is what it is the gradient of
+        if (p.softplus) dstep *= rcp_hw(1.0f + exp2_hw(-old.raw * kLog2e));
+        if (lane < rows) static_cast<T*>(p.ddelta)[(bi * p.L + t0 + lane) * p.H + h] = narrow<T>(dstep);
+        const float da = sum_wave(lane < rows ? dlog * old.step * a : 0.0f);
+        const float dbias = sum_wave(lane < rows ? dstep : 0.0f);
+        if (lane == 0) {
+            const int64_t at = (bi * p.chunks + ck) * p.H + h, one = p.b * p.chunks * p.H;
+            p.partial[at] = da;
+            p.partial[one + at] = dbias;
+            p.partial[2 * one + at] = d_sum;
+        }
+        to_sum = from_sum = w_sum = dot_sum = d_sum = 0.0f;
+    };
+
+    int h = h_first, slab = 0, prev_h = -1;
+    bool prev_done = false;
+    for (int it = 0; h < h_last; it++) {
+        const int buf = it % kGradBuffers<T>;
+        T* const x_lds = lds.x[buf];
+        T* const dy_lds = lds.dy[buf];
+        GateLds& gates = lds.gates[buf];
+        GradShares<NT>& shares = lds.shares[it & 1];
+        const int vcols = p.P - slab * kHeadSlab;
+        if (kGradBuffers<T> == 1) barrier_lds();
+        if (TileV::is_short(p.P, 0)) {
+            tx.load_short(xb + int64_t(h) * p.P, p.xt, rows, p.P);
+            ty.load_short(dyb + int64_t(h) * p.P, dyt, rows, p.P);
+        }
+        tx.store(x_lds, vcols, 0, rows, slab * kHeadSlab);
+        ty.store(dy_lds, vcols, 0, rows, slab * kHeadSlab);
+        if (wave == 0) {
+            old = gt;
+            old_a2 = a2;
+            a2 = a2_from_alog(p.A_log[h]);
+            bias = p.bias ? p.bias[h] : 0.0f;
+            gt = make_gate(Raw<T>::f(dl), bias, a2, p.softplus, lane < rows);
+            gates.put(gt);
+        }
+        barrier_lds();
+        const int next_slab = slab + 1 < p.slabs ? slab + 1 : 0, next_h = next_slab ? h : h + 1;
+        if (next_h < h_last) fetch(next_h, next_slab);
+        if (wave == 0 && prev_h >= 0) finish(lds.shares[(it & 1) ^ 1], prev_h, prev_done);
+
+        // Scores.
+        {
+            typename M::Frag yf[2], xf[2][2];
+#pragma unroll
+            for (int kk = 0; kk < 2; kk++) {
+                yf[kk] = M::load(dy_lds + (16 * si + lr) * kLdV + 32 * kk + 8 * lg);
+#pragma unroll
+                for (int k = 0; k < 2; k++)
+                    xf[k][kk] = M::load(x_lds + (16 * (sj + k) + lr) * kLdV + 32 * kk + 8 * lg);
+            }
+            const float* const ci = reinterpret_cast<const float*>(gates.c + 16 * si + 4 * lg);
+            const f32x4 c01 = floats4(ci), c23 = floats4(ci + 4);
+            f32x2 cj[2];
+            float sj_[2];
+#pragma unroll
+            for (int k = 0; k < 2; k++) {
+                cj[k] = gates.c[16 * (sj + k) + lr];
+                sj_[k] = gates.step[16 * (sj + k) + lr];
+            }
+            issue_loads<T>();
+            f32x4 row_sum = {0, 0, 0, 0};
+            float diag = 0.0f;
+#pragma unroll
+            for (int k = 0; k < 2; k++) {
+                const int jt = sj + k, j = 16 * jt + lr;
+                f32x4 gs = {0, 0, 0, 0}, ms, rs;
+#pragma unroll
+                for (int kk = 0; kk < 2; kk++) gs = M::mma(yf[kk], xf[k][kk], gs);
+                float col = 0.0f, on = 0.0f;
+#pragma unroll
+                for (int r = 0; r < 4; r++) {
+                    const int i = 16 * si + 4 * lg + r;
+                    const f32x4 cc = r < 2 ? c01 : c23;
+                    const float e = exp2_hw(c_diff(f32x2{cc[2 * (r & 1)], cc[2 * (r & 1) + 1]}, cj[k]));
+                    const float w = j <= i ? e : 0.0f;
+                    ms[r] = j <= i ? w * cb[k][r] : 0.0f;
+                    rs[r] = j <= i ? w * gs[r] * sj_[k] : 0.0f;
+                    const float pr = ms[r] * gs[r];
+                    const float below = j < i ? pr : 0.0f;
+                    col += below;
+                    row_sum[r] += below * sj_[k];
+                    on = j == i ? pr : on;
+                    diag += j == i ? gs[r] : 0.0f;
+                }
+                store4(lds.m + j * kLdV + 16 * si + 4 * lg, ms);
+                store4(lds.r + j * kLdV + 16 * si + 4 * lg, rs);
+                shares.col[4 * si + lg][j] = col;
+                if (jt == si && lr / 4 == lg) shares.diag[j] = on;
+            }
 #pragma unroll
             for (int r = 0; r < 4; r++) {
-                const int i = 16 * it + 4 * lg + r, n = n0 + 16 * nt;
-                if (i >= rows || n >= p.N) continue;
-                const int64_t at = ((bi * p.L + t0 + i) * p.G + g) * p.N + n;
-                if (p.blocks == 1) {
-                    static_cast<T*>(p.dB)[at] = narrow<T>(db[it][nt][r]);
-                    static_cast<T*>(p.dC)[at] = narrow<T>(dc[it][nt][r]);
+                const float v = sum_lanes16(row_sum[r]);
+                if (lr == 0) shares.row[wave & 1][16 * si + 4 * lg + r] = v;
+            }
+            diag = sum_wave(diag);
+            if (lane == 0) shares.dsum[wave] = diag;
+        }
+        // S and Q as operands; Q rounded for dx, by the waves that hold it first.
+        typename M::Frag sf[2][M::kWide], qf[2][M::kWide];
+        float dot = 0.0f;
+#pragma unroll
+        for (int kk = 0; kk < 2; kk++) {
+            M::split(sv[kk], sf[kk]);
+            M::split(qv[kk], qf[kk]);
+#pragma unroll
+            for (int e = 0; e < 8; e++) dot += sv[kk][e] * qv[kk][e];
+            if constexpr (sizeof(T) == 2)
+                if (it0 == 0) *reinterpret_cast<typename M::Frag*>(lds.q + n * kLdV + 32 * kk + 8 * lg) = qf[kk][0];
+        }
+        dot = sum_wave(dot);
+        if (lane == 0 && it0 == 0) shares.dot[nt] = dot;
+        if (next_h < h_last) fetch_states(next_h, next_slab);
+        barrier_lds();
+
+        // dC, dB and the state terms, a row tile at a time.
+#pragma unroll
+        for (int k = 0; k < ITW; k++) {
+            const int i0 = 16 * (it0 + k);
+            typename M::Frag yf[2], xf[2], rc[2], rr[2];
+            T cv[4], bv[4];
+#pragma unroll
+            for (int kk = 0; kk < 2; kk++) {
+                yf[kk] = M::load(dy_lds + (i0 + lr) * kLdV + 32 * kk + 8 * lg);
+                xf[kk] = M::load(x_lds + (i0 + lr) * kLdV + 32 * kk + 8 * lg);
+                rc[kk] = M::columns(lds.r, kLdV, 32 * kk, i0);
+                rr[kk] = M::load(lds.r + (i0 + lr) * kLdV + 32 * kk + 8 * lg);
+            }
+            const f32x4 in = floats4(gates.in + i0 + 4 * lg), rest = floats4(gates.rest + i0 + 4 * lg),
+                        st = floats4(gates.step + i0 + 4 * lg);
+#pragma unroll
+            for (int r = 0; r < 4; r++) {
+                cv[r] = lds.c[(i0 + 4 * lg + r) * kLdK + n];
+                bv[r] = lds.b[(i0 + 4 * lg + r) * kLdK + n];
+            }
+            issue_loads<T>();
+            f32x4 u = {0, 0, 0, 0}, v = {0, 0, 0, 0};
+#pragma unroll
+            for (int kk = 0; kk < 2; kk++) {
+                u = mma_wide<T>(yf[kk], sf[kk], u);
+                v = mma_wide<T>(xf[kk], qf[kk], v);
+            }
+            f32x4 yin, xin;
+#pragma unroll
+            for (int r = 0; r < 4; r++) {
+                const float ui = u[r] * in[r], vi = v[r] * rest[r];
+                yin[r] = sum_lanes16(ui * widen(cv[r]));
+                xin[r] = sum_lanes16(vi * widen(bv[r]));
+                dc[k][r] += ui;
+                db[k][r] += vi * st[r];
+            }
+#pragma unroll
+            for (int kk = 0; kk < 2; kk++) {
+                dc[k] = M::mma(rc[kk], bf[kk], dc[k]);
+                db[k] = M::mma(rr[kk], cf[kk], db[k]);
+            }
+            if (lr == 0) {
+                *reinterpret_cast<f32x4*>(&shares.yin[nt][i0 + 4 * lg]) = yin;
+                *reinterpret_cast<f32x4*>(&shares.xin[nt][i0 + 4 * lg]) = xin;
+            }
+        }
+
+        // dx.
+        {
+            typename M::Frag qb[NP / 32], yc[2];
+#pragma unroll
+            for (int kk = 0; kk < NP / 32; kk++) {
+                if constexpr (sizeof(T) == 2) {
+                    qb[kk] = M::columns(lds.q, kLdV, 32 * kk, dp - lr);
                 } else {
-                    const int64_t one = p.b * p.L * p.G * p.N;
-                    p.dbc[hb * one + at] = db[it][nt][r];
-                    p.dbc[(p.blocks + hb) * one + at] = dc[it][nt][r];
+                    const float* const q = p.chunk_q + state_at(h, slab) + (32 * kk + 8 * lg) * 64 + dp;
+#pragma unroll
+                    for (int e = 0; e < 8; e++) qb[kk][e] = q[e * 64];
                 }
             }
+#pragma unroll
+            for (int kk = 0; kk < 2; kk++) yc[kk] = M::columns(dy_lds, kLdV, 32 * kk, dp - lr);
+            const float skip = p.D[h];
+#pragma unroll
+            for (int k = 0; k < 2; k++) {
+                const int j0 = 16 * (dj + k);
+                typename M::Frag br[NP / 32], mr[2];
+                T yv[4];
+#pragma unroll
+                for (int kk = 0; kk < NP / 32; kk++) br[kk] = M::load(lds.b + (j0 + lr) * kLdK + 32 * kk + 8 * lg);
+#pragma unroll
+                for (int kk = 0; kk < 2; kk++) mr[kk] = M::load(lds.m + (j0 + lr) * kLdV + 32 * kk + 8 * lg);
+                const f32x4 out = floats4(gates.out + j0 + 4 * lg), st = floats4(gates.step + j0 + 4 * lg);
+#pragma unroll
+                for (int r = 0; r < 4; r++) yv[r] = dy_lds[(j0 + 4 * lg + r) * kLdV + dp];
+                issue_loads<T>();
+                f32x4 o = {0, 0, 0, 0}, q = {0, 0, 0, 0};
+#pragma unroll
+                for (int kk = 0; kk < NP / 32; kk++) q = M::mma(br[kk], qb[kk], q);
+#pragma unroll
+                for (int kk = 0; kk < 2; kk++) o = M::mma(mr[kk], yc[kk], o);
+                T* const dx = static_cast<T*>(p.dx) + (bi * p.L + t0 + j0 + 4 * lg) * dyt + int64_t(h) * p.P +
+                              slab * kHeadSlab + dp;
+#pragma unroll
+                for (int r = 0; r < 4; r++)
+                    if (j0 + 4 * lg + r < rows && dp < vcols)
+                        dx[r * dyt] = narrow<T>(o[r] * st[r] + q[r] * out[r] + skip * widen(yv[r]));
+            }
+        }
+        prev_h = h;
+        prev_done = next_slab == 0;
+        h = next_h;
+        slab = next_slab;
+    }
+    barrier_lds();
+    if (wave == 0) {
+        old = gt;
+        old_a2 = a2;
+        const int count = (h_last - h_first) * p.slabs;
+        finish(lds.shares[(count - 1) & 1], prev_h, true);
+    }
+#pragma unroll
+    for (int k = 0; k < ITW; k++)
+#pragma unroll
+        for (int r = 0; r < 4; r++) {
+            const int i = 16 * (it0 + k) + 4 * lg + r;
+            if (i >= rows || n >= p.N) continue;
+            const int64_t at = ((bi * p.L + t0 + i) * p.G + g) * p.N + n;
+            if (p.blocks == 1) {
+                static_cast<T*>(p.dB)[at] = narrow<T>(db[k][r]);
+                static_cast<T*>(p.dC)[at] = narrow<T>(dc[k][r]);
+            } else {
+                const int64_t one = p.b * p.L * p.G * p.N;
+                p.dbc[hb * one + at] = db[k][r];
+                p.dbc[(p.blocks + hb) * one + at] = dc[k][r];
+            }
+        }
 }
 
 // dB and dC from the head blocks' shares, in block order.
@@ -1063,7 +1136,7 @@ constexpr size_t head_out_lds() {
 }
 template <typename T, int NP>
 constexpr size_t head_grad_lds() {
-    return (2 * Tile<T, NP>::kElems + 4 * Tile<T, kHeadSlab>::kElems) * sizeof(T) + (5 * 64 + 3 * 256 + 8) * sizeof(float);
+    return sizeof(GradLds<T, NP>);
 }
 
 }  // namespace ss

@@ -153,6 +153,7 @@ int run_fwd(const HeadParams& p, hipStream_t st) {
 
 template <typename T, int NP, int JOBS>
 int run_bwd(HeadParams p, hipStream_t st) {
+    static_assert(ss::head_grad_lds<T, NP>() <= 160 * 1024, "LDS of a compute unit");
     constexpr size_t lds = ss::head_states_lds<T, NP, JOBS>();
     p.last = nullptr;
     if (p.nseg > 1) carry_segments<T, NP, JOBS, false>(p, st);
@@ -160,7 +161,7 @@ int run_bwd(HeadParams p, hipStream_t st) {
     if (p.nseg > 1) carry_segments<T, NP, JOBS, true>(p, st);
     ss::head_states<T, NP, JOBS, true, StateMode::Chunks><<<walkers(p, JOBS), 256, lds, st>>>(p);
     const unsigned grid = unsigned(p.b * p.chunks * p.G * p.blocks);
-    ss::head_grad<T, NP><<<grid, 256, ss::head_grad_lds<T, NP>(), st>>>(p);
+    ss::head_grad<T, NP><<<grid, 512, ss::head_grad_lds<T, NP>(), st>>>(p);
     if (p.blocks > 1) {
         const int64_t items = 2 * p.b * p.L * p.G * p.N;
         ss::head_sum_blocks<T><<<unsigned(std::min<int64_t>((items + 255) / 256, 1 << 20)), 256, 0, st>>>(p);
