@@ -47,9 +47,8 @@ template <> struct Mat<uint16_t> {
     // The operand whose k are the LDS tile's rows k0 .. k0 + 31, for column c0 + lane % 16: two transposing reads.
     // Each takes 4 rows of 16 columns from a group of 16 lanes, which name 4 columns of a row apiece, and gives
     // every lane its column's 4 rows.
-    static __device__ __forceinline__ Frag columns(const uint16_t* tile, int ld, int k0, int c0) {
+    static __device__ __forceinline__ Frag columns(const uint16_t* tile, int ld, int k0, int c0, int lane) {
         typedef short s16x4 __attribute__((ext_vector_type(4)));
-        const int lane = threadIdx.x & 63;
         const uint16_t* const p = tile + (k0 + lane / 16 * 8 + lane % 16 / 4) * ld + c0 + lane % 4 * 4;
         auto* const q = (__attribute__((address_space(3))) s16x4*)(p);
         auto* const r = (__attribute__((address_space(3))) s16x4*)(p + 4 * ld);
@@ -98,8 +97,7 @@ template <> struct Mat<float> {
         const f32x4 a = *reinterpret_cast<const f32x4*>(p), b = *reinterpret_cast<const f32x4*>(q);
         return Frag{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
     }
-    static __device__ __forceinline__ Frag columns(const float* tile, int ld, int k0, int c0) {
-        const int lane = threadIdx.x & 63;
+    static __device__ __forceinline__ Frag columns(const float* tile, int ld, int k0, int c0, int lane) {
         const float* const p = tile + (k0 + lane / 16 * 8) * ld + c0 + lane % 16;
         Frag v;
 #pragma unroll
@@ -115,6 +113,20 @@ template <> struct Mat<float> {
         return c;
     }
 };
+
+// This lane's number, opaque to the optimiser: what is derived from it inside
+// a loop is formed there, in a few instructions, and does not take registers
+// for the whole loop (hoisted LDS addresses cost head_grad 50 spilled ones).
+__device__ __forceinline__ int fresh_lane() {
+    int lane = int(threadIdx.x & 63);
+    asm volatile("" : "+v"(lane));
+    return lane;
+}
+__device__ __forceinline__ int fresh_thread() {
+    int thread = int(threadIdx.x);
+    asm volatile("" : "+v"(thread));
+    return thread;
+}
 
 // a * (f[0] + f[1] + ...), the small parts first.
 template <typename T>
@@ -182,33 +194,35 @@ struct Tile {
     static_assert(64 * kPerRow % THREADS == 0, "whole vectors per thread");
     u32x4 v[kN];
 
-    static __device__ __forceinline__ int row0() { return int(threadIdx.x) / kPerRow; }
-    static __device__ __forceinline__ int col0() { return int(threadIdx.x) % kPerRow * kVec; }
+    static __device__ __forceinline__ int row0(int thread) { return thread / kPerRow; }
+    static __device__ __forceinline__ int col0(int thread) { return thread % kPerRow * kVec; }
 
     // Rows `stride` elements apart (64 of them span less than 2^32 bytes), `before` elements of the same row before
     // src.  Rows shorter than a vector are left to load_short(), called when the tile is stored.
     static __device__ __forceinline__ bool is_short(int cols, int before) { return cols + before < kVec; }
     __device__ __forceinline__ void load(const T* src, int64_t stride, int rows, int cols, int before = 0) {
+        const int thread = fresh_thread(), row0 = this->row0(thread), col0 = this->col0(thread);
         const int last = cols - kVec, shift = min(0, last);   // the last vector's column, and where the first one starts
         const char* const from = reinterpret_cast<const char*>(src + shift);
         const uint32_t step = uint32_t(stride) * uint32_t(sizeof(T));
-        const uint32_t col = uint32_t(min(col0(), last) - shift) * uint32_t(sizeof(T));
+        const uint32_t col = uint32_t(min(col0, last) - shift) * uint32_t(sizeof(T));
         uint32_t off[kN];   // bytes
         if (rows == 64) {
 #pragma unroll
-            for (int i = 0; i < kN; i++) off[i] = uint32_t(row0()) * step + col + uint32_t(i * kRowStep) * step;
+            for (int i = 0; i < kN; i++) off[i] = uint32_t(row0) * step + col + uint32_t(i * kRowStep) * step;
         } else {
 #pragma unroll
-            for (int i = 0; i < kN; i++) off[i] = uint32_t(min(row0() + i * kRowStep, rows - 1)) * step + col;
+            for (int i = 0; i < kN; i++) off[i] = uint32_t(min(row0 + i * kRowStep, rows - 1)) * step + col;
         }
         if (!is_short(cols, before))
 #pragma unroll
             for (int i = 0; i < kN; i++) v[i] = load16(reinterpret_cast<const T*>(from + off[i]));
     }
     __device__ __forceinline__ void load_short(const T* src, int64_t stride, int rows, int cols) {
+        const int row0 = this->row0(int(threadIdx.x));
 #pragma unroll
         for (int i = 0; i < kN; i++) {
-            const T* const p = src + min(row0() + i * kRowStep, rows - 1) * stride;
+            const T* const p = src + min(row0 + i * kRowStep, rows - 1) * stride;
             v[i] = u32x4{0, 0, 0, 0};
 #pragma unroll
             for (int e = 0; e < kVec - 1; e++)
@@ -220,13 +234,14 @@ struct Tile {
     }
     // To LDS: rows lo .. hi - 1, and zeros in the others' place.
     __device__ __forceinline__ void store(T* lds, int cols, int lo, int hi, int before = 0) const {
-        T* const q = lds + row0() * kLd + col0();
+        const int thread = fresh_thread(), row0 = this->row0(thread), col0 = this->col0(thread);
+        T* const q = lds + row0 * kLd + col0;
         if (lo == 0 && hi == 64 && cols >= COLS) {
 #pragma unroll
             for (int i = 0; i < kN; i++) *reinterpret_cast<u32x4*>(q + i * kRowStep * kLd) = v[i];
         } else {
             // A partial vector was loaded from `late` elements before its place.
-            const int late = !is_short(cols, before) ? max(0, col0() + kVec - cols) : col0() < cols ? 0 : kVec;
+            const int late = !is_short(cols, before) ? max(0, col0 + kVec - cols) : col0 < cols ? 0 : kVec;
             const int bits = late * 8 * int(sizeof(T));
 #pragma unroll
             for (int i = 0; i < kN; i++) {
@@ -238,7 +253,7 @@ struct Tile {
                     a = a >> bits | b << (64 - bits);
                     b >>= bits;
                 }
-                const int row = row0() + i * kRowStep;
+                const int row = row0 + i * kRowStep;
                 const bool in = row >= lo && row < hi;
                 const u32x4 w = {uint32_t(a), uint32_t(a >> 32), uint32_t(b), uint32_t(b >> 32)}, zero = {0, 0, 0, 0};
                 *reinterpret_cast<u32x4*>(q + i * kRowStep * kLd) = in ? w : zero;
@@ -247,8 +262,9 @@ struct Tile {
     }
     // The tile's rows lo .. hi - 1 and columns inside, from LDS to memory.
     static __device__ __forceinline__ void write(const T* lds, T* dst, int64_t stride, int lo, int hi, int cols) {
-        T* const p = dst + row0() * stride + col0();
-        const T* const q = lds + row0() * kLd + col0();
+        const int thread = fresh_thread(), row0 = Tile::row0(thread), col0 = Tile::col0(thread);
+        T* const p = dst + row0 * stride + col0;
+        const T* const q = lds + row0 * kLd + col0;
         if (lo == 0 && hi == 64 && cols >= COLS) {
 #pragma unroll
             for (int i = 0; i < kN; i++)
@@ -257,13 +273,13 @@ struct Tile {
         }
 #pragma unroll
         for (int i = 0; i < kN; i++)
-            if (row0() + i * kRowStep >= lo && row0() + i * kRowStep < hi) {
-                if (col0() + kVec <= cols) {
+            if (row0 + i * kRowStep >= lo && row0 + i * kRowStep < hi) {
+                if (col0 + kVec <= cols) {
                     store16(p + i * kRowStep * stride, *reinterpret_cast<const u32x4*>(q + i * kRowStep * kLd));
                 } else {
 #pragma unroll
                     for (int e = 0; e < kVec - 1; e++)
-                        if (col0() + e < cols) p[i * kRowStep * stride + e] = q[i * kRowStep * kLd + e];
+                        if (col0 + e < cols) p[i * kRowStep * stride + e] = q[i * kRowStep * kLd + e];
                 }
             }
     }

@@ -218,14 +218,15 @@ __device__ __forceinline__ void state_load(f32x4 (&acc)[JOBS][NP / 16], const fl
 }
 template <int NP, int JOBS>
 __device__ __forceinline__ void state_store(const f32x4 (&acc)[JOBS][NP / 16], float* dst, int p0) {
-    const int lane = threadIdx.x & 63;
+    const int lane = fresh_lane();
+    dst += lane / 16 * 256 + p0 + lane % 16;
 #pragma unroll
     for (int ct = 0; ct < JOBS; ct++)
 #pragma unroll
         for (int nt = 0; nt < NP / 16; nt++)
 #pragma unroll
             for (int r = 0; r < 4; r++)
-                dst[(16 * nt + lane / 16 * 4 + r) * 64 + p0 + 16 * ct + lane % 16] = acc[ct][nt][r];
+                dst[(16 * nt + r) * 64 + 16 * ct] = acc[ct][nt][r];
 }
 // The same from / to a (b, H, P, N) tensor; NULL reads as zero.
 template <int NP, int JOBS>
@@ -261,10 +262,11 @@ __device__ __forceinline__ void state_write(const f32x4 (&acc)[JOBS][NP / 16], c
 // tile [step][channel], w the steps' weights.
 template <typename T, int NP, int JOBS>
 __device__ __forceinline__ void state_update(f32x4 (&acc)[JOBS][NP / 16], float decay, const T* k_lds,
-                                             const typename Mat<T>::Frag (&vf)[JOBS][2], const float* weights) {
+                                             const typename Mat<T>::Frag (&vf)[JOBS][2], const float* weights,
+                                             int lane) {
     using M = Mat<T>;
     constexpr int kLd = Tile<T, NP>::kLd;
-    const int lg = (threadIdx.x & 63) >> 4;
+    const int lg = lane >> 4;
     f32x8 wv[2];
 #pragma unroll
     for (int kk = 0; kk < 2; kk++) wv[kk] = floats8(weights + 32 * kk + 8 * lg);
@@ -275,7 +277,7 @@ __device__ __forceinline__ void state_update(f32x4 (&acc)[JOBS][NP / 16], float 
 #pragma unroll
         for (int k = 0; k < 4; k++) {
             const int at = 4 * i + k;
-            kf[i & 1][k] = M::columns(k_lds, kLd, at / (NP / 16) * 32, at % (NP / 16) * 16);
+            kf[i & 1][k] = M::columns(k_lds, kLd, at / (NP / 16) * 32, at % (NP / 16) * 16, lane);
         }
     };
     load_k(0);
@@ -360,6 +362,7 @@ __global__ __launch_bounds__(256, 2) void head_states(HeadParams p) {
     float total = 0.0f;
     Steps steps;
     for (int it = 0; it < count;) {
+        const int lane = fresh_lane();
         const int ck = REV ? w.last - it : w.first + it, rows = chunk_rows(p, ck);
         barrier_lds();
         if (min(p.N, p.P) < TileK::kVec) fetch_short(ck, rows);
@@ -387,11 +390,11 @@ __global__ __launch_bounds__(256, 2) void head_states(HeadParams p) {
         for (int ct = 0; ct < JOBS; ct++)
 #pragma unroll
             for (int kk = 0; kk < 2; kk++)
-                vf[ct][kk] = M::columns(v_lds + w.job * TileV::kElems, TileV::kLd, 32 * kk, w.p0 + 16 * ct);
+                vf[ct][kk] = M::columns(v_lds + w.job * TileV::kElems, TileV::kLd, 32 * kk, w.p0 + 16 * ct, lane);
         const GateLds& gt = gates[w.job];
         const float cq = gt.c[63].x;
         total += cq;
-        state_update<T, NP, JOBS>(acc, exp2_hw(cq), k_lds, vf, REV ? gt.in : gt.out);
+        state_update<T, NP, JOBS>(acc, exp2_hw(cq), k_lds, vf, REV ? gt.in : gt.out, lane);
         if (done) it++;
     }
     if (!w.my_alive) return;
@@ -450,7 +453,7 @@ __global__ __launch_bounds__(256, 2) void head_out(HeadParams p) {
     GateLds* const gates = reinterpret_cast<GateLds*>(m_lds + JOBS * TileV::kElems);
 
     const Walk<JOBS> w(p);
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, lr = lane & 15, lg = lane >> 4;
+    const int wave = threadIdx.x >> 6;
     const int gate_head = w.gate_head();
     const T* const bb = static_cast<const T*>(p.B) + w.bi * p.Bb + int64_t(w.g) * p.N;
     const T* const cb = static_cast<const T*>(p.C) + w.bi * p.Cb + int64_t(w.g) * p.N;
@@ -505,6 +508,7 @@ __global__ __launch_bounds__(256, 2) void head_out(HeadParams p) {
     Steps steps;
     int out_ck = -1, out_lo = 0, out_hi = 0;   // the outputs in x_lds
     for (int ck = w.first; ck <= w.last;) {
+        const int lane = fresh_lane(), lr = lane & 15, lg = lane >> 4;
         const int rows = chunk_rows(p, ck);
         barrier_lds();
         if (out_ck >= 0) write_y(out_ck, out_lo, out_hi);
@@ -565,7 +569,7 @@ __global__ __launch_bounds__(256, 2) void head_out(HeadParams p) {
 #pragma unroll
         for (int ct = 0; ct < JOBS; ct++)
 #pragma unroll
-            for (int kk = 0; kk < 2; kk++) xf[ct][kk] = M::columns(xj, TileV::kLd, 32 * kk, w.p0 + 16 * ct);
+            for (int kk = 0; kk < 2; kk++) xf[ct][kk] = M::columns(xj, TileV::kLd, 32 * kk, w.p0 + 16 * ct, lane);
         load_c(0);
         issue_loads<T>();
 #pragma unroll
@@ -642,7 +646,7 @@ __global__ __launch_bounds__(256, 2) void head_out(HeadParams p) {
             for (int k = 0; k < 16; k++)
                 at[(k / 4 * 16 + k % 4) * TileV::kLd] = narrow<T>(out[ct][k / 4][k % 4] + skip * widen(xd[k]));
         }
-        state_update<T, NP, JOBS>(acc, exp2_hw(gt.c[63].x), b_lds, xf, gt.out);
+        state_update<T, NP, JOBS>(acc, exp2_hw(gt.c[63].x), b_lds, xf, gt.out, lane);
         if (done) ck++;
     }
     barrier_lds();
@@ -718,7 +722,7 @@ __global__ __launch_bounds__(512, 2) void head_grad(HeadParams p) {
     const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
     const int si = wave >> 1, sj = 2 * (wave & 1);            // score tiles (si, sj) and (si, sj + 1)
     const int nt = wave % NT, it0 = wave / NT * ITW;          // columns and row tiles of dB and dC
-    const int dp = 16 * (wave & 3) + lr, dj = 2 * (wave >> 2);   // column and row tiles of dx
+    const int dj = 2 * (wave >> 2);   // row tiles of dx
     const int n = 16 * nt + lr;
     const int64_t t0 = int64_t(ck) * kHeadChunk;
     const int rows = chunk_rows(p, ck), per_group = p.H / p.G;
@@ -779,8 +783,8 @@ __global__ __launch_bounds__(512, 2) void head_grad(HeadParams p) {
     typename M::Frag bf[2], cf[2];   // B and C as operands, steps by column n
 #pragma unroll
     for (int kk = 0; kk < 2; kk++) {
-        bf[kk] = M::columns(lds.b, kLdK, 32 * kk, 16 * nt);
-        cf[kk] = M::columns(lds.c, kLdK, 32 * kk, 16 * nt);
+        bf[kk] = M::columns(lds.b, kLdK, 32 * kk, 16 * nt, lane);
+        cf[kk] = M::columns(lds.c, kLdK, 32 * kk, 16 * nt, lane);
     }
     f32x4 db[ITW], dc[ITW];
 #pragma unroll
@@ -790,7 +794,7 @@ __global__ __launch_bounds__(512, 2) void head_grad(HeadParams p) {
     float to_sum = 0.0f, from_sum = 0.0f, w_sum = 0.0f, dot_sum = 0.0f, d_sum = 0.0f;
     Gate gt{}, old{};
     float a2 = 0.0f, bias = 0.0f, old_a2 = 0.0f;
-    auto finish = [&](const GradShares<NT>& sh, int h, bool done) {
+    auto finish = [&](const GradShares<NT>& sh, int h, bool done, int lane) {
         float yi = 0.0f, xi = 0.0f, ci = 0.0f;
 #pragma unroll
         for (int k = 0; k < NT; k++) {
@@ -836,6 +840,8 @@ __global__ __launch_bounds__(512, 2) void head_grad(HeadParams p) {
     int h = h_first, slab = 0, prev_h = -1;
     bool prev_done = false;
     for (int it = 0; h < h_last; it++) {
+        const int lane = fresh_lane(), lr = lane & 15, lg = lane >> 4, n = 16 * nt + lr;
+        const int dp = 16 * (wave & 3) + lr;   // column of dx
         const int buf = it % kGradBuffers<T>;
         T* const x_lds = lds.x[buf];
         T* const dy_lds = lds.dy[buf];
@@ -860,7 +866,7 @@ __global__ __launch_bounds__(512, 2) void head_grad(HeadParams p) {
         barrier_lds();
         const int next_slab = slab + 1 < p.slabs ? slab + 1 : 0, next_h = next_slab ? h : h + 1;
         if (next_h < h_last) fetch(next_h, next_slab);
-        if (wave == 0 && prev_h >= 0) finish(lds.shares[(it & 1) ^ 1], prev_h, prev_done);
+        if (wave == 0 && prev_h >= 0) finish(lds.shares[(it & 1) ^ 1], prev_h, prev_done, lane);
 
         // Scores.
         {
@@ -946,7 +952,7 @@ __global__ __launch_bounds__(512, 2) void head_grad(HeadParams p) {
             for (int kk = 0; kk < 2; kk++) {
                 yf[kk] = M::load(dy_lds + (i0 + lr) * kLdV + 32 * kk + 8 * lg);
                 xf[kk] = M::load(x_lds + (i0 + lr) * kLdV + 32 * kk + 8 * lg);
-                rc[kk] = M::columns(lds.r, kLdV, 32 * kk, i0);
+                rc[kk] = M::columns(lds.r, kLdV, 32 * kk, i0, lane);
                 rr[kk] = M::load(lds.r + (i0 + lr) * kLdV + 32 * kk + 8 * lg);
             }
             const f32x4 in = floats4(gates.in + i0 + 4 * lg), rest = floats4(gates.rest + i0 + 4 * lg),
@@ -989,7 +995,7 @@ __global__ __launch_bounds__(512, 2) void head_grad(HeadParams p) {
 #pragma unroll
             for (int kk = 0; kk < NP / 32; kk++) {
                 if constexpr (sizeof(T) == 2) {
-                    qb[kk] = M::columns(lds.q, kLdV, 32 * kk, dp - lr);
+                    qb[kk] = M::columns(lds.q, kLdV, 32 * kk, dp - lr, lane);
                 } else {
                     const float* const q = p.chunk_q + state_at(h, slab) + (32 * kk + 8 * lg) * 64 + dp;
 #pragma unroll
@@ -997,7 +1003,7 @@ __global__ __launch_bounds__(512, 2) void head_grad(HeadParams p) {
                 }
             }
 #pragma unroll
-            for (int kk = 0; kk < 2; kk++) yc[kk] = M::columns(dy_lds, kLdV, 32 * kk, dp - lr);
+            for (int kk = 0; kk < 2; kk++) yc[kk] = M::columns(dy_lds, kLdV, 32 * kk, dp - lr, lane);
             const float skip = p.D[h];
 #pragma unroll
             for (int k = 0; k < 2; k++) {
@@ -1035,7 +1041,7 @@ __global__ __launch_bounds__(512, 2) void head_grad(HeadParams p) {
         old = gt;
         old_a2 = a2;
         const int count = (h_last - h_first) * p.slabs;
-        finish(lds.shares[(count - 1) & 1], prev_h, true);
+        finish(lds.shares[(count - 1) & 1], prev_h, true, lane);
     }
 #pragma unroll
     for (int k = 0; k < ITW; k++)
