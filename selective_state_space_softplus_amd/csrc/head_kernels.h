@@ -35,6 +35,7 @@ struct HeadParams {
     int H, P, N, G;
     int slabs, chunks;      // ceil(P / 64), ceil(L / 64)
     int nseg, seg_chunks;   // segments of the sequence, chunks in each but the last
+    int jobs;               // (head, slab) pairs of a walking workgroup
     int softplus;
     float *seg_state;       // (b, H, slabs, nseg, NP, 64): the segments' states
     float *seg_decay;       // (b, H, nseg): log2 of the segments' decays
@@ -154,14 +155,14 @@ struct Walk {
     int first, last;             // chunks
     int p0;                      // this wave's first channel in the slab
 
-    __device__ __forceinline__ explicit Walk(const HeadParams& p) {
+    __device__ __forceinline__ Walk(const HeadParams& p, int nseg, int first_seg) {
         const int heads = p.H / p.G, jobs = heads * p.slabs, blocks = (jobs + JOBS - 1) / JOBS;
         const uint32_t piece = piece_of(blockIdx.x, gridDim.x);
         const int at = int(piece % uint32_t(p.G * blocks));
         const uint32_t rest = piece / uint32_t(p.G * blocks);
         g = at / blocks;
-        seg = int(rest % uint32_t(p.nseg));
-        bi = rest / uint32_t(p.nseg);
+        seg = first_seg + int(rest % uint32_t(nseg));
+        bi = rest / uint32_t(nseg);
 #pragma unroll
         for (int k = 0; k < JOBS; k++) {
             const int q = at % blocks * JOBS + k, in = min(q, jobs - 1);
@@ -309,8 +310,8 @@ enum class StateMode { Local, Chunks };
 //   REV true:  the adjoint state Q backwards, Q = exp(c_63) Q' + sum_i exp(c_i) dy_i C_i^T.
 //   Local:  a segment's state from zero, to seg_state, and its decay to seg_decay.
 //   Chunks: from seg_state (several segments) or the given end state; the state
-//           at entry to every chunk goes to chunk_s or chunk_q, the last one to
-//           last / dh0 where a segment is the whole sequence.
+//           at entry to every chunk goes to chunk_s or chunk_q, the adjoint one
+//           past the sequence's start to dh0.
 template <typename T, int NP, int JOBS, bool REV, StateMode MODE>
 __global__ __launch_bounds__(256, 2) void head_states(HeadParams p) {
     using M = Mat<T>;
@@ -321,7 +322,8 @@ __global__ __launch_bounds__(256, 2) void head_states(HeadParams p) {
     T* const v_lds = k_lds + TileK::kElems;
     GateLds* const gates = reinterpret_cast<GateLds*>(v_lds + JOBS * TileV::kElems);
 
-    const Walk<JOBS> w(p);
+    // The last segment of the walk has no Local pass: nothing starts from its state.
+    const Walk<JOBS> w(p, MODE == StateMode::Local ? p.nseg - 1 : p.nseg, MODE == StateMode::Local && REV ? 1 : 0);
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int gate_head = w.gate_head();
     const T* const kb = REV ? static_cast<const T*>(p.C) + w.bi * p.Cb + int64_t(w.g) * p.N
@@ -401,14 +403,14 @@ __global__ __launch_bounds__(256, 2) void head_states(HeadParams p) {
     if (MODE == StateMode::Local) {
         state_store<NP, JOBS>(acc, seg_at, w.p0);
         if (w.my_slab == 0 && lane == 0) p.seg_decay[(w.bi * p.H + w.my_h) * p.nseg + w.seg] = total;
-    } else if (p.nseg == 1 && (REV ? p.dh0 : p.last)) {
-        state_write<NP, JOBS>(acc, p, w, REV ? p.dh0 : p.last);
+    } else if (REV && w.seg == 0 && p.dh0) {
+        state_write<NP, JOBS>(acc, p, w, p.dh0);
     }
 }
 
 // The segments' states from zero, in place, become the states at the segments'
 // starts (REV: the adjoint states at their ends), walking from the given end
-// state; what is left past the last one goes to last / dh0.
+// state.
 template <int NP, bool REV>
 __global__ __launch_bounds__(256) void head_carry(HeadParams p) {
     const int64_t at = int64_t(blockIdx.x) * 256 + threadIdx.x;   // (b, h, slab, n, channel)
@@ -424,15 +426,13 @@ __global__ __launch_bounds__(256) void head_carry(HeadParams p) {
     for (int i = 0; i < p.nseg; i++) {
         const int seg = REV ? p.nseg - 1 - i : i;
         float* const q = states + int64_t(seg) * (NP * 64);
-        const float local = *q;
+        const float next = i + 1 < p.nseg ? exp2_hw(p.seg_decay[bh * p.nseg + seg]) * s + *q : 0.0f;
         *q = s;
-        s = exp2_hw(p.seg_decay[bh * p.nseg + seg]) * s + local;
+        s = next;
     }
-    float* const out = REV ? p.dh0 : p.last;
-    if (out && inside) out[(bh * p.P + pg) * p.N + n] = s;
 }
 
-// The outputs of a segment, and with one segment the last state.
+// The outputs of a segment, and the last state from the last one.
 //
 // Per chunk: the scores B C^T, formed once for the workgroup's pairs and
 // weighted for each, go through LDS as the first operand of the product with x;
@@ -452,7 +452,7 @@ __global__ __launch_bounds__(256, 2) void head_out(HeadParams p) {
     T* const m_lds = x_lds + JOBS * TileV::kElems;    // weighted scores [i][j]
     GateLds* const gates = reinterpret_cast<GateLds*>(m_lds + JOBS * TileV::kElems);
 
-    const Walk<JOBS> w(p);
+    const Walk<JOBS> w(p, p.nseg, 0);
     const int wave = threadIdx.x >> 6;
     const int gate_head = w.gate_head();
     const T* const bb = static_cast<const T*>(p.B) + w.bi * p.Bb + int64_t(w.g) * p.N;
@@ -651,7 +651,7 @@ __global__ __launch_bounds__(256, 2) void head_out(HeadParams p) {
     }
     barrier_lds();
     write_y(out_ck, out_lo, out_hi);
-    if (p.nseg == 1 && p.last && w.my_alive) state_write<NP, JOBS>(acc, p, w, p.last);
+    if (w.seg == p.nseg - 1 && p.last && w.my_alive) state_write<NP, JOBS>(acc, p, w, p.last);
 }
 
 // Gradients of one chunk for the heads of one head block of a group.

@@ -34,20 +34,33 @@ int check_shape(const Shape& s, int dtype) {
 // The state's rows as the kernels pad them.
 int64_t padded_state(int64_t N, bool grad) { return N <= 32 && !grad ? 32 : N <= 64 ? 64 : 128; }
 
-// Segments of the sequence that are walked over at the same time.  A walk over
-// one (row, head, slab) is one workgroup; where those are fewer than twice the
-// compute units, the sequence is split so that they are not, down to two
-// chunks a segment, at the cost of a first pass over x and B for the states
-// at the segments' starts.
-constexpr int64_t kWantedPieces = 512;
+// (Head, slab) pairs to a workgroup of a walk: two halve its LDS reads; fp32
+// fragments leave no registers for it, and a group with one pair has no second.
+int64_t jobs_of(const Shape& s, int dtype) { return dtype == SS_BF16 && s.H / s.G * s.slabs() > 1 ? 2 : 1; }
 
-int64_t segment_chunks(const Shape& s) {
-    const int64_t base = s.b * s.H * s.slabs(), chunks = s.chunks();
-    const int64_t segs = std::max<int64_t>(1, std::min((kWantedPieces + base - 1) / base, chunks / 2));
-    return (chunks + segs - 1) / segs;
+// Workgroups of a walk over one segment of every sequence.
+int64_t walkers_of(const Shape& s, int dtype) {
+    const int64_t jobs = jobs_of(s, dtype);
+    return s.b * s.G * ((s.H / s.G * s.slabs() + jobs - 1) / jobs);
 }
 
-int64_t segments(const Shape& s) { return (s.chunks() + segment_chunks(s) - 1) / segment_chunks(s); }
+// Segments of the sequence that are walked over at the same time: as many as
+// make all their workgroups resident at once (two to each of 256 compute
+// units), down to one chunk a segment.  More would start a second, mostly
+// empty round: forward b = 4, L = 8192, H = 80 (160 walkers) takes 632 us with 3
+// segments, 746 with 4, 770 with 1; b = 1, L = 16384, H = 80 (40) 379 us with 12,
+// 408 with 16, 438 with 6; b = 1, L = 777, H = 24 (12) 27 us with 13, 72 with 1.
+// The cost is a first pass over x and B for the states at the segments' starts.
+constexpr int64_t kResident = 512;
+
+int64_t segment_chunks(const Shape& s, int dtype) {
+    const int64_t segs = std::max<int64_t>(1, std::min(kResident / walkers_of(s, dtype), s.chunks()));
+    return (s.chunks() + segs - 1) / segs;
+}
+
+int64_t segments(const Shape& s, int dtype) {
+    return (s.chunks() + segment_chunks(s, dtype) - 1) / segment_chunks(s, dtype);
+}
 
 // Heads of a group whose shares of dB and dC one workgroup of the backward
 // adds up: all of them, unless that leaves fewer than 1024 workgroups.
@@ -61,9 +74,9 @@ struct Workspace {
     size_t seg_state, seg_decay, chunk_s, chunk_q, partial, dbc, total;
 };
 
-Workspace layout(const Shape& s, bool grad) {
+Workspace layout(const Shape& s, int dtype, bool grad) {
     const size_t np = size_t(padded_state(s.N, grad)) * 64 * sizeof(float);
-    const size_t walks = size_t(s.b * s.H * s.slabs()), nseg = size_t(segments(s));
+    const size_t walks = size_t(s.b * s.H * s.slabs()), nseg = size_t(segments(s, dtype));
     Workspace w{};
     size_t at = 0;
     auto take = [&](size_t& field, size_t bytes) {
@@ -99,7 +112,7 @@ int64_t extent(const Shape& s, int64_t sb, int64_t st, int64_t inner) {
     return n <= kMaxElems ? n : -1;
 }
 
-HeadParams params_of(const Shape& s, const Strides& st, void* ws, bool grad) {
+HeadParams params_of(const Shape& s, const Strides& st, int dtype, void* ws, bool grad) {
     HeadParams p{};
     p.b = s.b;
     p.L = s.L;
@@ -109,8 +122,9 @@ HeadParams params_of(const Shape& s, const Strides& st, void* ws, bool grad) {
     p.G = int(s.G);
     p.slabs = int(s.slabs());
     p.chunks = int(s.chunks());
-    p.seg_chunks = int(segment_chunks(s));
-    p.nseg = int(segments(s));
+    p.seg_chunks = int(segment_chunks(s, dtype));
+    p.nseg = int(segments(s, dtype));
+    p.jobs = int(jobs_of(s, dtype));
     p.xb = st.xb;
     p.xt = st.xt;
     p.deltab = st.db;
@@ -119,7 +133,7 @@ HeadParams params_of(const Shape& s, const Strides& st, void* ws, bool grad) {
     p.Bt = st.Bt;
     p.Cb = st.Cb;
     p.Ct = st.Ct;
-    const Workspace w = layout(s, grad);
+    const Workspace w = layout(s, dtype, grad);
     char* const at = static_cast<char*>(ws);
     p.seg_state = reinterpret_cast<float*>(at + w.seg_state);
     p.seg_decay = reinterpret_cast<float*>(at + w.seg_decay);
@@ -132,22 +146,24 @@ HeadParams params_of(const Shape& s, const Strides& st, void* ws, bool grad) {
     return p;
 }
 
-// Workgroups of a walk over the sequence that take `jobs` (head, slab) pairs of a group each.
-unsigned walkers(const HeadParams& p, int jobs) {
-    return unsigned(p.b * p.nseg * p.G * ((p.H / p.G * p.slabs + jobs - 1) / jobs));
+// Workgroups of a walk over `nseg` segments that take `jobs` (head, slab) pairs of a group each.
+unsigned walkers(const HeadParams& p, int jobs, int nseg) {
+    return unsigned(p.b * nseg * p.G * ((p.H / p.G * p.slabs + jobs - 1) / jobs));
 }
 
+// The states at the segments' starts (REV: the adjoint states at their ends).  The last segment of the walk needs
+// no pass of its own.
 template <typename T, int NP, int JOBS, bool REV>
 void carry_segments(const HeadParams& p, hipStream_t st) {
     ss::head_states<T, NP, JOBS, REV, StateMode::Local>
-        <<<walkers(p, JOBS), 256, ss::head_states_lds<T, NP, JOBS>(), st>>>(p);
+        <<<walkers(p, JOBS, p.nseg - 1), 256, ss::head_states_lds<T, NP, JOBS>(), st>>>(p);
     ss::head_carry<NP, REV><<<unsigned(p.b * p.H * p.slabs) * (NP * 64 / 256), 256, 0, st>>>(p);
 }
 
 template <typename T, int NP, int JOBS>
 int run_fwd(const HeadParams& p, hipStream_t st) {
     if (p.nseg > 1) carry_segments<T, NP, JOBS, false>(p, st);
-    ss::head_out<T, NP, JOBS><<<walkers(p, JOBS), 256, ss::head_out_lds<T, NP, JOBS>(), st>>>(p);
+    ss::head_out<T, NP, JOBS><<<walkers(p, JOBS, p.nseg), 256, ss::head_out_lds<T, NP, JOBS>(), st>>>(p);
     return status(hipGetLastError());
 }
 
@@ -155,11 +171,10 @@ template <typename T, int NP, int JOBS>
 int run_bwd(HeadParams p, hipStream_t st) {
     static_assert(ss::head_grad_lds<T, NP>() <= 160 * 1024, "LDS of a compute unit");
     constexpr size_t lds = ss::head_states_lds<T, NP, JOBS>();
-    p.last = nullptr;
     if (p.nseg > 1) carry_segments<T, NP, JOBS, false>(p, st);
-    ss::head_states<T, NP, JOBS, false, StateMode::Chunks><<<walkers(p, JOBS), 256, lds, st>>>(p);
+    ss::head_states<T, NP, JOBS, false, StateMode::Chunks><<<walkers(p, JOBS, p.nseg), 256, lds, st>>>(p);
     if (p.nseg > 1) carry_segments<T, NP, JOBS, true>(p, st);
-    ss::head_states<T, NP, JOBS, true, StateMode::Chunks><<<walkers(p, JOBS), 256, lds, st>>>(p);
+    ss::head_states<T, NP, JOBS, true, StateMode::Chunks><<<walkers(p, JOBS, p.nseg), 256, lds, st>>>(p);
     const unsigned grid = unsigned(p.b * p.chunks * p.G * p.blocks);
     ss::head_grad<T, NP><<<grid, 512, ss::head_grad_lds<T, NP>(), st>>>(p);
     if (p.blocks > 1) {
@@ -170,24 +185,17 @@ int run_bwd(HeadParams p, hipStream_t st) {
     return status(hipGetLastError());
 }
 
-// Pairs to a workgroup: two halve its LDS reads; fp32 fragments leave no
-// registers for it, and a group with one pair has no second.
-template <typename T>
-bool two_jobs(const HeadParams& p) {
-    return sizeof(T) == 2 && p.H / p.G * p.slabs > 1;
-}
-
 template <typename T, int NP>
 int fwd_jobs(const HeadParams& p, hipStream_t st) {
     if constexpr (sizeof(T) == 2)
-        if (two_jobs<T>(p)) return run_fwd<T, NP, 2>(p, st);
+        if (p.jobs == 2) return run_fwd<T, NP, 2>(p, st);
     return run_fwd<T, NP, 1>(p, st);
 }
 
 template <typename T, int NP>
 int bwd_jobs(const HeadParams& p, hipStream_t st) {
     if constexpr (sizeof(T) == 2)
-        if (two_jobs<T>(p)) return run_bwd<T, NP, 2>(p, st);
+        if (p.jobs == 2) return run_bwd<T, NP, 2>(p, st);
     return run_bwd<T, NP, 1>(p, st);
 }
 
@@ -241,13 +249,13 @@ int run_step(float* state, const void* x, const void* dt, const float* A_log, co
 SS_EXPORT size_t ss_head_scan_fwd_workspace_bytes(int64_t b, int64_t L, int64_t H, int64_t P, int64_t N, int64_t G,
                                                   int dtype) {
     const Shape s{b, L, H, P, N, G};
-    return check_shape(s, dtype) == SS_OK ? layout(s, false).total : 0;
+    return check_shape(s, dtype) == SS_OK ? layout(s, dtype, false).total : 0;
 }
 
 SS_EXPORT size_t ss_head_scan_bwd_workspace_bytes(int64_t b, int64_t L, int64_t H, int64_t P, int64_t N, int64_t G,
                                                   int dtype) {
     const Shape s{b, L, H, P, N, G};
-    return check_shape(s, dtype) == SS_OK ? layout(s, true).total : 0;
+    return check_shape(s, dtype) == SS_OK ? layout(s, dtype, true).total : 0;
 }
 
 SS_EXPORT int ss_head_scan_fwd(const void* x, const void* delta, const float* A_log, const void* B, const void* C,
@@ -274,14 +282,14 @@ SS_EXPORT int ss_head_scan_fwd(const void* x, const void* delta, const float* A_
                          same(rh, rl) ? Range{0, 0} : rh};
     const Range outs[] = {range_of(y, b * L * H * P, es), rl};
     if (!apart(ins, outs) || overlaps(rh, outs[0])) return SS_ERR_ALIAS;
-    const size_t need = layout(s, false).total;
+    const size_t need = layout(s, dtype, false).total;
     if (need) {
         if (!workspace || workspace_bytes < need) return SS_ERR_WORKSPACE;
         if (!aligned(workspace, 256)) return SS_ERR_ALIGN;
         const Range rw[] = {range_of(workspace, int64_t(need), 1)};
         if (!apart(ins, rw) || !apart(outs, rw) || overlaps(rh, rw[0])) return SS_ERR_ALIAS;
     }
-    HeadParams p = params_of(s, st, workspace, false);
+    HeadParams p = params_of(s, st, dtype, workspace, false);
     p.x = x;
     p.delta = delta;
     p.A_log = A_log;
@@ -328,12 +336,12 @@ SS_EXPORT int ss_head_scan_bwd(const void* x, const void* delta, const float* A_
                           range_of(dB, nb, es), range_of(dC, nb, es), range_of(dD, H, 4),
                           range_of(ddelta_bias, H, 4), range_of(dinitial_state, ns, 4)};
     if (!apart(ins, outs)) return SS_ERR_ALIAS;
-    const size_t need = layout(s, true).total;
+    const size_t need = layout(s, dtype, true).total;
     if (!workspace || workspace_bytes < need) return SS_ERR_WORKSPACE;
     if (!aligned(workspace, 256)) return SS_ERR_ALIGN;
     const Range rw[] = {range_of(workspace, int64_t(need), 1)};
     if (!apart(ins, rw) || !apart(outs, rw)) return SS_ERR_ALIAS;
-    HeadParams p = params_of(s, st, workspace, true);
+    HeadParams p = params_of(s, st, dtype, workspace, true);
     p.x = x;
     p.delta = delta;
     p.A_log = A_log;
