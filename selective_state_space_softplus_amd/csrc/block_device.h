@@ -137,6 +137,15 @@ __device__ __forceinline__ f32x4 mma_wide(typename Mat<T>::Frag a, const typenam
     return c;
 }
 
+// (f[0] + f[1] + ...) * b.
+template <typename T>
+__device__ __forceinline__ f32x4 wide_mma(const typename Mat<T>::Frag (&f)[Mat<T>::kWide], typename Mat<T>::Frag b,
+                                          f32x4 c) {
+#pragma unroll
+    for (int i = Mat<T>::kWide - 1; i >= 0; i--) c = Mat<T>::mma(f[i], b, c);
+    return c;
+}
+
 // Keeps the loads before it before the products after it: left to itself the
 // compiler puts each LDS load right before its product and waits for each
 // (~100 cycles, 72 of them per chunk in head_out).  Only with bf16, whose
@@ -151,6 +160,33 @@ __device__ __forceinline__ void store4(uint16_t* p, f32x4 v) {
     *reinterpret_cast<u32x2*>(p) = u32x2{f32x2_to_bf16x2(v[0], v[1]), f32x2_to_bf16x2(v[2], v[3])};
 }
 __device__ __forceinline__ void store4(float* p, f32x4 v) { *reinterpret_cast<f32x4*>(p) = v; }
+__device__ __forceinline__ f32x4 load4(const uint16_t* p) {
+    const u32x2 v = *reinterpret_cast<const u32x2*>(p);
+    return f32x4{__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u), __uint_as_float(v.y << 16),
+                 __uint_as_float(v.y & 0xffff0000u)};
+}
+__device__ __forceinline__ f32x4 load4(const float* p) { return *reinterpret_cast<const f32x4*>(p); }
+// 4 values to global memory at any element's address.
+__device__ __forceinline__ void store4_any(uint16_t* p, f32x4 v) {
+    typedef u32x2 V __attribute__((aligned(2)));
+    *reinterpret_cast<V*>(p) = u32x2{f32x2_to_bf16x2(v[0], v[1]), f32x2_to_bf16x2(v[2], v[3])};
+}
+__device__ __forceinline__ void store4_any(float* p, f32x4 v) {
+    typedef f32x4 V __attribute__((aligned(4)));
+    *reinterpret_cast<V*>(p) = v;
+}
+
+// The same for a lane whose row has `left` elements from p on.
+template <typename T>
+__device__ __forceinline__ void store_left(T* p, f32x4 v, int left) {
+    if (left >= 4) {
+        store4_any(p, v);
+    } else {
+#pragma unroll
+        for (int r = 0; r < 3; r++)
+            if (r < left) Elem<T>::store(p, r, v[r]);
+    }
+}
 
 template <typename T>
 __device__ __forceinline__ float widen(T v) {
@@ -300,7 +336,12 @@ __device__ __forceinline__ double dpp_or_zero(double v) {
     const uint32_t hi = uint32_t(__builtin_amdgcn_update_dpp(0, int(uint32_t(u >> 32)), CTRL, ROWS, 0xf, false));
     return __builtin_bit_cast(double, uint64_t(hi) << 32 | lo);
 }
-__device__ __forceinline__ double running_sum(double v) {
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float dpp_or_zero(float v) {
+    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, ROWS, 0xf, false));
+}
+template <typename V>
+__device__ __forceinline__ V running_sum(V v) {
     v += dpp_or_zero<0x111, 0xf>(v);   // row_shr:1
     v += dpp_or_zero<0x112, 0xf>(v);
     v += dpp_or_zero<0x114, 0xf>(v);
@@ -327,6 +368,14 @@ __device__ __forceinline__ float sum_groups4(float v) {
     return v + __shfl_xor(v, 32);
 }
 __device__ __forceinline__ float sum_wave(float v) { return sum_groups4(sum_lanes16(v)); }
+
+// Sums over the 4 lane groups of two values: a's in the first two groups'
+// lanes, b's in the others'.  Swapping halves adds both at once.
+__device__ __forceinline__ float sum_groups4_pair(float a, float b) {
+    const auto h = __builtin_amdgcn_permlane32_swap(__float_as_uint(a), __float_as_uint(b), false, false);
+    const float v = __uint_as_float(h[0]) + __uint_as_float(h[1]);
+    return v + __shfl_xor(v, 16);
+}
 
 // Workgroups are handed to the 8 XCDs in turn.  With `total` of them, the
 // workgroup `id` takes piece piece_of(id, total): each XCD then holds one

@@ -77,6 +77,9 @@ __device__ __forceinline__ Gate make_gate(float delta, float bias, float a2, int
     return g;
 }
 
+// The value of the last lane of each row of 16.
+__device__ __forceinline__ float dpp_row_last(float v) { return __shfl(v, (threadIdx.x & 63) | 15); }
+
 // A chunk's gates in LDS.
 struct GateLds {
     f32x2 c[64];      // running sums
@@ -84,6 +87,8 @@ struct GateLds {
     float in[64];     // exp(c_t): from the state before the chunk to step t
     float rest[64];   // exp(c_63 - c_t): from step t to the state after the chunk
     float out[64];    // the same times s_t: from x_t
+    float tail[64];   // exp(c_e - c_t) s_t with e the last of t's 16 steps
+    float raw[64];    // the step size's argument
     uint32_t flags[4];
 
     // By one wave.
@@ -94,8 +99,12 @@ struct GateLds {
         c[lane] = g.c;
         step[lane] = g.step;
         in[lane] = exp2_hw(g.c.x);
-        rest[lane] = exp2_hw(c_diff(cq, g.c));
-        out[lane] = rest[lane] * g.step;
+        const float left = exp2_hw(c_diff(cq, g.c));
+        rest[lane] = left;
+        out[lane] = left * g.step;
+        raw[lane] = g.raw;
+        const f32x2 ce = {dpp_row_last(g.c.x), dpp_row_last(g.c.y)};
+        tail[lane] = exp2_hw(c_diff(ce, g.c)) * g.step;
     }
 };
 
@@ -453,7 +462,7 @@ __global__ __launch_bounds__(256, 2) void head_out(HeadParams p) {
     GateLds* const gates = reinterpret_cast<GateLds*>(m_lds + JOBS * TileV::kElems);
 
     const Walk<JOBS> w(p, p.nseg, 0);
-    const int wave = threadIdx.x >> 6;
+    const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
     const int gate_head = w.gate_head();
     const T* const bb = static_cast<const T*>(p.B) + w.bi * p.Bb + int64_t(w.g) * p.N;
     const T* const cb = static_cast<const T*>(p.C) + w.bi * p.Cb + int64_t(w.g) * p.N;
@@ -554,7 +563,8 @@ __global__ __launch_bounds__(256, 2) void head_out(HeadParams p) {
                 if (kk + 1 < KN) load_bc(kk + 1);
                 issue_loads<T>();
 #pragma unroll
-                for (int jt = 0; jt < 4; jt++) sc[jt] = M::mma(bj[kk & 1][jt], ci[kk & 1], sc[jt]);
+                for (int jt = 0; jt < 4; jt++)
+                    if (jt <= wave) sc[jt] = M::mma(bj[kk & 1][jt], ci[kk & 1], sc[jt]);
             }
         }
         // What the readout needs besides the scores.
@@ -572,32 +582,38 @@ __global__ __launch_bounds__(256, 2) void head_out(HeadParams p) {
             for (int kk = 0; kk < 2; kk++) xf[ct][kk] = M::columns(xj, TileV::kLd, 32 * kk, w.p0 + 16 * ct, lane);
         load_c(0);
         issue_loads<T>();
+        // Weighted: exp(c_i - c_j) s_j as exp(c_i - c_e) tail_j with e the last step of tile jt < it, neither above 1.
 #pragma unroll
         for (int k = 0; k < JOBS; k++) {
             const f32x2 ci = gates[k].c[i_row];
-            f32x4 c01[4], c23[4], sj[4];
+            const float* const cj = reinterpret_cast<const float*>(gates[k].c + 16 * wave + 4 * lg);
+            const f32x4 c01 = floats4(cj), c23 = floats4(cj + 4), sj = floats4(gates[k].step + 16 * wave + 4 * lg);
+            f32x2 ce[3];
+            f32x4 tail[3];
 #pragma unroll
-            for (int jt = 0; jt < 4; jt++) {
-                const float* const cj = reinterpret_cast<const float*>(gates[k].c + 16 * jt + 4 * lg);
-                c01[jt] = floats4(cj);
-                c23[jt] = floats4(cj + 4);
-                sj[jt] = floats4(gates[k].step + 16 * jt + 4 * lg);
+            for (int jt = 0; jt < 3; jt++) {
+                ce[jt] = gates[k].c[16 * jt + 15];
+                tail[jt] = floats4(gates[k].tail + 16 * jt + 4 * lg);
             }
             issue_loads<T>();
+            T* const mi = m_lds + k * TileV::kElems + i_row * TileV::kLd + 4 * lg;
 #pragma unroll
             for (int jt = 0; jt < 4; jt++) {
-                f32x4 m;
+                f32x4 m = {0, 0, 0, 0};
+                if (jt < 3 && jt < wave) {
+                    m = sc[jt] * tail[jt] * exp2_hw(c_diff(ci, ce[jt]));
+                } else if (jt == wave) {
 #pragma unroll
-                for (int r = 0; r < 4; r++) {
-                    const f32x4 cc = r < 2 ? c01[jt] : c23[jt];
-                    const float e = exp2_hw(c_diff(ci, f32x2{cc[2 * (r & 1)], cc[2 * (r & 1) + 1]}));
-                    const float v = sc[jt][r] * (e * sj[jt][r]);
-                    m[r] = 16 * jt + 4 * lg + r <= i_row ? v : 0.0f;
+                    for (int r = 0; r < 4; r++) {
+                        const f32x4 cc = r < 2 ? c01 : c23;
+                        const float e = exp2_hw(c_diff(ci, f32x2{cc[2 * (r & 1)], cc[2 * (r & 1) + 1]}));
+                        m[r] = 4 * lg + r <= lr ? sc[jt][r] * (e * sj[r]) : 0.0f;
+                    }
                 }
-                store4(m_lds + k * TileV::kElems + i_row * TileV::kLd + 16 * jt + 4 * lg, m);
+                store4(mi + 16 * jt, m);
             }
         }
-        f32x4 out[JOBS][4];
+        f32x4 out[JOBS][4];   // channels p0 + 16 ct + 4 lg + r of rows 16 it + lr
 #pragma unroll
         for (int ct = 0; ct < JOBS; ct++)
 #pragma unroll
@@ -611,12 +627,12 @@ __global__ __launch_bounds__(256, 2) void head_out(HeadParams p) {
                 const f32x4 u = acc[ct][2 * kk], v = acc[ct][2 * kk + 1];
                 const typename M::Frag sf = M::pack(f32x8{u[0], u[1], u[2], u[3], v[0], v[1], v[2], v[3]});
 #pragma unroll
-                for (int it = 0; it < 4; it++) out[ct][it] = M::mma(cf[kk & 1][it], sf, out[ct][it]);
+                for (int it = 0; it < 4; it++) out[ct][it] = M::mma(sf, cf[kk & 1][it], out[ct][it]);
             }
         }
 #pragma unroll
         for (int it = 0; it < 4; it++) {
-            const f32x4 ein = floats4(gt.in + 16 * it + 4 * lg);
+            const float ein = gt.in[16 * it + lr];
 #pragma unroll
             for (int ct = 0; ct < JOBS; ct++) out[ct][it] *= ein;
         }
@@ -634,17 +650,16 @@ __global__ __launch_bounds__(256, 2) void head_out(HeadParams p) {
 #pragma unroll
             for (int kk = 0; kk <= it / 2; kk++)
 #pragma unroll
-                for (int ct = 0; ct < JOBS; ct++) out[ct][it] = M::mma(mf[it][kk], xf[ct][kk], out[ct][it]);
+                for (int ct = 0; ct < JOBS; ct++) out[ct][it] = M::mma(xf[ct][kk], mf[it][kk], out[ct][it]);
 #pragma unroll
         for (int ct = 0; ct < JOBS; ct++) {
-            T* const at = xj + 4 * lg * TileV::kLd + w.p0 + 16 * ct + lr;
-            T xd[16];
+            T* const at = xj + lr * TileV::kLd + w.p0 + 16 * ct + 4 * lg;
+            f32x4 xd[4];
 #pragma unroll
-            for (int k = 0; k < 16; k++) xd[k] = at[(k / 4 * 16 + k % 4) * TileV::kLd];
+            for (int it = 0; it < 4; it++) xd[it] = load4(at + 16 * it * TileV::kLd);
             issue_loads<T>();
 #pragma unroll
-            for (int k = 0; k < 16; k++)
-                at[(k / 4 * 16 + k % 4) * TileV::kLd] = narrow<T>(out[ct][k / 4][k % 4] + skip * widen(xd[k]));
+            for (int it = 0; it < 4; it++) store4(at + 16 * it * TileV::kLd, out[ct][it] + skip * xd[it]);
         }
         state_update<T, NP, JOBS>(acc, exp2_hw(gt.c[63].x), b_lds, xf, gt.out, lane);
         if (done) ck++;
@@ -697,7 +712,7 @@ struct GradLds {
     T x[kGradBuffers<T>][kTileV], dy[kGradBuffers<T>][kTileV];
     T m[kTileV], r[kTileV];                                // L_ij (C_i . B_j) and R_ij as [j][i]
     T q[sizeof(T) == 2 ? NP * Tile<T, kHeadSlab>::kLd : 8];   // Q rounded, [n][channel]
-    GateLds gates[kGradBuffers<T>];
+    GateLds gates[2];
     GradShares<NP / 16> shares[2];
 };
 
@@ -792,9 +807,9 @@ __global__ __launch_bounds__(512, 2) void head_grad(HeadParams p) {
 
     // Sums over the slabs of a head (wave 0, lane t), and what its ddelta takes.
     float to_sum = 0.0f, from_sum = 0.0f, w_sum = 0.0f, dot_sum = 0.0f, d_sum = 0.0f;
-    Gate gt{}, old{};
-    float a2 = 0.0f, bias = 0.0f, old_a2 = 0.0f;
-    auto finish = [&](const GradShares<NT>& sh, int h, bool done, int lane) {
+    constexpr int kGateWave = 4;
+    auto finish = [&](const GradShares<NT>& sh, const GateLds& gt, int h, bool done, int lane) {
+        const float step = gt.step[lane], raw = gt.raw[lane], decay = gt.in[63];
         float yi = 0.0f, xi = 0.0f, ci = 0.0f;
 #pragma unroll
         for (int k = 0; k < NT; k++) {
@@ -808,27 +823,21 @@ __global__ __launch_bounds__(512, 2) void head_grad(HeadParams p) {
             if (k < NT) dot_sum += sh.dot[k];
             d_sum += sh.dsum[k];
         }
-        to_sum += sh.row[0][lane] + sh.row[1][lane] - old.step * ci + yi;
-        from_sum += old.step * xi;
+        to_sum += sh.row[0][lane] + sh.row[1][lane] - step * ci + yi;
+        from_sum += step * xi;
         w_sum += sh.diag[lane] + ci + xi;
         if (!done) return;
-        float to = to_sum, from = from_sum;   // sums over steps >= t, and < t
-#pragma unroll
-        for (int m = 1; m < 64; m <<= 1) {
-            const float down = __shfl_down(to, m), up = __shfl_up(from, m);
-            to += lane + m < 64 ? down : 0.0f;
-            from += lane >= m ? up : 0.0f;
-        }
-        from = __shfl_up(from, 1);
-        const float decay = exp2_hw(__int_as_float(__builtin_amdgcn_readlane(__float_as_int(old.c.x), 63)));
-        const float dlog = to + (lane > 0 ? from : 0.0f) + decay * dot_sum;
-        const float a = old_a2 * kLn2;
+        // Sums over steps >= t (a running sum in reverse), and < t.
+        const float to = __shfl(running_sum(__shfl(to_sum, 63 - lane)), 63 - lane);
+        const float from = dpp<0x138>(running_sum(from_sum));   // wave_shr:1, 0 into lane 0
+        const float a = a2_from_alog(p.A_log[h]) * kLn2;
+        const float dlog = to + from + decay * dot_sum;
         float dstep = a * dlog + w_sum;   // w_sum lacks the step: it is what it is the gradient of
-        if (p.softplus) dstep *= rcp_hw(1.0f + exp2_hw(-old.raw * kLog2e));
+        if (p.softplus) dstep *= rcp_hw(1.0f + exp2_hw(-raw * kLog2e));
         if (lane < rows) static_cast<T*>(p.ddelta)[(bi * p.L + t0 + lane) * p.H + h] = narrow<T>(dstep);
-        const float da = sum_wave(lane < rows ? dlog * old.step * a : 0.0f);
-        const float dbias = sum_wave(lane < rows ? dstep : 0.0f);
-        if (lane == 0) {
+        const float da = running_sum(lane < rows ? dlog * step * a : 0.0f);
+        const float dbias = running_sum(lane < rows ? dstep : 0.0f);
+        if (lane == 63) {
             const int64_t at = (bi * p.chunks + ck) * p.H + h, one = p.b * p.chunks * p.H;
             p.partial[at] = da;
             p.partial[one + at] = dbias;
@@ -841,11 +850,11 @@ __global__ __launch_bounds__(512, 2) void head_grad(HeadParams p) {
     bool prev_done = false;
     for (int it = 0; h < h_last; it++) {
         const int lane = fresh_lane(), lr = lane & 15, lg = lane >> 4, n = 16 * nt + lr;
-        const int dp = 16 * (wave & 3) + lr;   // column of dx
+        const int dp = 16 * (wave & 3);   // first column of dx
         const int buf = it % kGradBuffers<T>;
         T* const x_lds = lds.x[buf];
         T* const dy_lds = lds.dy[buf];
-        GateLds& gates = lds.gates[buf];
+        GateLds& gates = lds.gates[it & 1];
         GradShares<NT>& shares = lds.shares[it & 1];
         const int vcols = p.P - slab * kHeadSlab;
         if (kGradBuffers<T> == 1) barrier_lds();
@@ -855,18 +864,13 @@ __global__ __launch_bounds__(512, 2) void head_grad(HeadParams p) {
         }
         tx.store(x_lds, vcols, 0, rows, slab * kHeadSlab);
         ty.store(dy_lds, vcols, 0, rows, slab * kHeadSlab);
-        if (wave == 0) {
-            old = gt;
-            old_a2 = a2;
-            a2 = a2_from_alog(p.A_log[h]);
-            bias = p.bias ? p.bias[h] : 0.0f;
-            gt = make_gate(Raw<T>::f(dl), bias, a2, p.softplus, lane < rows);
-            gates.put(gt);
-        }
+        if (wave == kGateWave)
+            gates.put(make_gate(Raw<T>::f(dl), p.bias ? p.bias[h] : 0.0f, a2_from_alog(p.A_log[h]), p.softplus,
+                                lane < rows));
         barrier_lds();
         const int next_slab = slab + 1 < p.slabs ? slab + 1 : 0, next_h = next_slab ? h : h + 1;
         if (next_h < h_last) fetch(next_h, next_slab);
-        if (wave == 0 && prev_h >= 0) finish(lds.shares[(it & 1) ^ 1], prev_h, prev_done, lane);
+        if (wave == 0 && prev_h >= 0) finish(lds.shares[(it & 1) ^ 1], lds.gates[(it & 1) ^ 1], prev_h, prev_done, lane);
 
         // Scores.
         {
@@ -947,7 +951,6 @@ __global__ __launch_bounds__(512, 2) void head_grad(HeadParams p) {
         for (int k = 0; k < ITW; k++) {
             const int i0 = 16 * (it0 + k);
             typename M::Frag yf[2], xf[2], rc[2], rr[2];
-            T cv[4], bv[4];
 #pragma unroll
             for (int kk = 0; kk < 2; kk++) {
                 yf[kk] = M::load(dy_lds + (i0 + lr) * kLdV + 32 * kk + 8 * lg);
@@ -955,37 +958,27 @@ __global__ __launch_bounds__(512, 2) void head_grad(HeadParams p) {
                 rc[kk] = M::columns(lds.r, kLdV, 32 * kk, i0, lane);
                 rr[kk] = M::load(lds.r + (i0 + lr) * kLdV + 32 * kk + 8 * lg);
             }
-            const f32x4 in = floats4(gates.in + i0 + 4 * lg), rest = floats4(gates.rest + i0 + 4 * lg),
-                        st = floats4(gates.step + i0 + 4 * lg);
-#pragma unroll
-            for (int r = 0; r < 4; r++) {
-                cv[r] = lds.c[(i0 + 4 * lg + r) * kLdK + n];
-                bv[r] = lds.b[(i0 + 4 * lg + r) * kLdK + n];
-            }
+            const float in = gates.in[i0 + lr], rest = gates.rest[i0 + lr], out = gates.out[i0 + lr];
+            const f32x4 cv = load4(lds.c + (i0 + lr) * kLdK + 16 * nt + 4 * lg),
+                        bv = load4(lds.b + (i0 + lr) * kLdK + 16 * nt + 4 * lg);
             issue_loads<T>();
-            f32x4 u = {0, 0, 0, 0}, v = {0, 0, 0, 0};
+            f32x4 u = {0, 0, 0, 0}, v = {0, 0, 0, 0};   // rows n = 16 nt + 4 lg + r of column i0 + lr
 #pragma unroll
             for (int kk = 0; kk < 2; kk++) {
-                u = mma_wide<T>(yf[kk], sf[kk], u);
-                v = mma_wide<T>(xf[kk], qf[kk], v);
+                u = wide_mma<T>(sf[kk], yf[kk], u);
+                v = wide_mma<T>(qf[kk], xf[kk], v);
             }
-            f32x4 yin, xin;
-#pragma unroll
-            for (int r = 0; r < 4; r++) {
-                const float ui = u[r] * in[r], vi = v[r] * rest[r];
-                yin[r] = sum_lanes16(ui * widen(cv[r]));
-                xin[r] = sum_lanes16(vi * widen(bv[r]));
-                dc[k][r] += ui;
-                db[k][r] += vi * st[r];
-            }
+            const f32x4 uc = u * cv, vb = v * bv;
+            const float sums = sum_groups4_pair(((uc[0] + uc[1]) + (uc[2] + uc[3])) * in,
+                                                ((vb[0] + vb[1]) + (vb[2] + vb[3])) * rest);
+            if (lg == 0) shares.yin[nt][i0 + lr] = sums;
+            if (lg == 2) shares.xin[nt][i0 + lr] = sums;
+            dc[k] += u * in;
+            db[k] += v * out;
 #pragma unroll
             for (int kk = 0; kk < 2; kk++) {
-                dc[k] = M::mma(rc[kk], bf[kk], dc[k]);
-                db[k] = M::mma(rr[kk], cf[kk], db[k]);
-            }
-            if (lr == 0) {
-                *reinterpret_cast<f32x4*>(&shares.yin[nt][i0 + 4 * lg]) = yin;
-                *reinterpret_cast<f32x4*>(&shares.xin[nt][i0 + 4 * lg]) = xin;
+                dc[k] = M::mma(bf[kk], rc[kk], dc[k]);
+                db[k] = M::mma(cf[kk], rr[kk], db[k]);
             }
         }
 
@@ -995,40 +988,36 @@ __global__ __launch_bounds__(512, 2) void head_grad(HeadParams p) {
 #pragma unroll
             for (int kk = 0; kk < NP / 32; kk++) {
                 if constexpr (sizeof(T) == 2) {
-                    qb[kk] = M::columns(lds.q, kLdV, 32 * kk, dp - lr, lane);
+                    qb[kk] = M::columns(lds.q, kLdV, 32 * kk, dp, lane);
                 } else {
-                    const float* const q = p.chunk_q + state_at(h, slab) + (32 * kk + 8 * lg) * 64 + dp;
+                    const float* const q = p.chunk_q + state_at(h, slab) + (32 * kk + 8 * lg) * 64 + dp + lr;
 #pragma unroll
                     for (int e = 0; e < 8; e++) qb[kk][e] = q[e * 64];
                 }
             }
 #pragma unroll
-            for (int kk = 0; kk < 2; kk++) yc[kk] = M::columns(dy_lds, kLdV, 32 * kk, dp - lr, lane);
+            for (int kk = 0; kk < 2; kk++) yc[kk] = M::columns(dy_lds, kLdV, 32 * kk, dp, lane);
             const float skip = p.D[h];
 #pragma unroll
             for (int k = 0; k < 2; k++) {
                 const int j0 = 16 * (dj + k);
                 typename M::Frag br[NP / 32], mr[2];
-                T yv[4];
 #pragma unroll
                 for (int kk = 0; kk < NP / 32; kk++) br[kk] = M::load(lds.b + (j0 + lr) * kLdK + 32 * kk + 8 * lg);
 #pragma unroll
                 for (int kk = 0; kk < 2; kk++) mr[kk] = M::load(lds.m + (j0 + lr) * kLdV + 32 * kk + 8 * lg);
-                const f32x4 out = floats4(gates.out + j0 + 4 * lg), st = floats4(gates.step + j0 + 4 * lg);
-#pragma unroll
-                for (int r = 0; r < 4; r++) yv[r] = dy_lds[(j0 + 4 * lg + r) * kLdV + dp];
+                const float out = gates.out[j0 + lr], st = gates.step[j0 + lr];
+                const f32x4 yv = load4(dy_lds + (j0 + lr) * kLdV + dp + 4 * lg);
                 issue_loads<T>();
-                f32x4 o = {0, 0, 0, 0}, q = {0, 0, 0, 0};
+                f32x4 o = {0, 0, 0, 0}, q = {0, 0, 0, 0};   // channels dp + 4 lg + r of row j0 + lr
 #pragma unroll
-                for (int kk = 0; kk < NP / 32; kk++) q = M::mma(br[kk], qb[kk], q);
+                for (int kk = 0; kk < NP / 32; kk++) q = M::mma(qb[kk], br[kk], q);
 #pragma unroll
-                for (int kk = 0; kk < 2; kk++) o = M::mma(mr[kk], yc[kk], o);
-                T* const dx = static_cast<T*>(p.dx) + (bi * p.L + t0 + j0 + 4 * lg) * dyt + int64_t(h) * p.P +
-                              slab * kHeadSlab + dp;
-#pragma unroll
-                for (int r = 0; r < 4; r++)
-                    if (j0 + 4 * lg + r < rows && dp < vcols)
-                        dx[r * dyt] = narrow<T>(o[r] * st[r] + q[r] * out[r] + skip * widen(yv[r]));
+                for (int kk = 0; kk < 2; kk++) o = M::mma(yc[kk], mr[kk], o);
+                const f32x4 d = o * st + q * out + skip * yv;
+                T* const dx = static_cast<T*>(p.dx) + (bi * p.L + t0 + j0 + lr) * dyt + int64_t(h) * p.P +
+                              slab * kHeadSlab + dp + 4 * lg;
+                if (j0 + lr < rows) store_left(dx, d, vcols - (dp + 4 * lg));
             }
         }
         prev_h = h;
@@ -1038,27 +1027,23 @@ __global__ __launch_bounds__(512, 2) void head_grad(HeadParams p) {
     }
     barrier_lds();
     if (wave == 0) {
-        old = gt;
-        old_a2 = a2;
-        const int count = (h_last - h_first) * p.slabs;
-        finish(lds.shares[(count - 1) & 1], prev_h, true, lane);
+        const int at = ((h_last - h_first) * p.slabs - 1) & 1;
+        finish(lds.shares[at], lds.gates[at], prev_h, true, lane);
     }
 #pragma unroll
-    for (int k = 0; k < ITW; k++)
-#pragma unroll
-        for (int r = 0; r < 4; r++) {
-            const int i = 16 * (it0 + k) + 4 * lg + r;
-            if (i >= rows || n >= p.N) continue;
-            const int64_t at = ((bi * p.L + t0 + i) * p.G + g) * p.N + n;
-            if (p.blocks == 1) {
-                static_cast<T*>(p.dB)[at] = narrow<T>(db[k][r]);
-                static_cast<T*>(p.dC)[at] = narrow<T>(dc[k][r]);
-            } else {
-                const int64_t one = p.b * p.L * p.G * p.N;
-                p.dbc[hb * one + at] = db[k][r];
-                p.dbc[(p.blocks + hb) * one + at] = dc[k][r];
-            }
+    for (int k = 0; k < ITW; k++) {
+        const int i = 16 * (it0 + k) + lr;
+        if (i >= rows) continue;
+        const int64_t at = ((bi * p.L + t0 + i) * p.G + g) * p.N, one = p.b * p.L * p.G * p.N;
+        const int left = p.N - (16 * nt + 4 * lg);   // columns from this lane's first
+        if (p.blocks == 1) {
+            store_left(static_cast<T*>(p.dB) + at + 16 * nt + 4 * lg, db[k], left);
+            store_left(static_cast<T*>(p.dC) + at + 16 * nt + 4 * lg, dc[k], left);
+        } else {
+            store_left(p.dbc + hb * one + at + 16 * nt + 4 * lg, db[k], left);
+            store_left(p.dbc + (p.blocks + hb) * one + at + 16 * nt + 4 * lg, dc[k], left);
         }
+    }
 }
 
 // dB and dC from the head blocks' shares, in block order.
