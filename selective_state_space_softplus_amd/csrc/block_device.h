@@ -34,7 +34,6 @@ template <typename T> struct Mat;
 
 template <> struct Mat<uint16_t> {
     using Frag = bf16x8;
-    static constexpr int kWide = 3;
     // 8 consecutive elements at p (16-byte aligned).
     static __device__ __forceinline__ Frag load(const uint16_t* p) {
         return __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4*>(p));
@@ -71,14 +70,15 @@ template <> struct Mat<uint16_t> {
         }
         return o;
     }
-    // An fp32 operand as three bf16 ones whose sum it is: 8 + 8 + 8 bits of
-    // its 24 (each remainder is exact), so products with an exact bf16 operand
-    // sum to what fp32 multiplication would.
-    static __device__ __forceinline__ void split(f32x8 v, Frag (&f)[3]) {
+    // An fp32 operand as a sum of bf16 ones (each remainder is exact).  Three
+    // hold 8 + 8 + 8 bits, all of it: products with an exact bf16 operand then
+    // sum to what fp32 multiplication would.  Two leave 2^-18 of it at most.
+    template <int PARTS>
+    static __device__ __forceinline__ void split(f32x8 v, Frag (&f)[PARTS]) {
 #pragma unroll
-        for (int i = 0; i < 3; i++) {
+        for (int i = 0; i < PARTS; i++) {
             f[i] = pack(v);
-            if (i < 2) v -= unpack(f[i]);
+            if (i + 1 < PARTS) v -= unpack(f[i]);
         }
     }
     static __device__ __forceinline__ f32x4 mma(Frag a, Frag b, f32x4 c) {
@@ -88,7 +88,6 @@ template <> struct Mat<uint16_t> {
 
 template <> struct Mat<float> {
     using Frag = f32x8;
-    static constexpr int kWide = 1;
     static __device__ __forceinline__ Frag load(const float* p) {
         const f32x4 a = *reinterpret_cast<const f32x4*>(p), b = *reinterpret_cast<const f32x4*>(p + 4);
         return Frag{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
@@ -106,7 +105,11 @@ template <> struct Mat<float> {
     }
     static __device__ __forceinline__ Frag pack(f32x8 v) { return v; }
     static __device__ __forceinline__ f32x8 unpack(Frag f) { return f; }
-    static __device__ __forceinline__ void split(f32x8 v, Frag (&f)[1]) { f[0] = v; }
+    template <int PARTS>
+    static __device__ __forceinline__ void split(f32x8 v, Frag (&f)[PARTS]) {
+        static_assert(PARTS == 1, "fp32 operands are whole");
+        f[0] = v;
+    }
     static __device__ __forceinline__ f32x4 mma(Frag a, Frag b, f32x4 c) {
 #pragma unroll
         for (int i = 0; i < 8; i++) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[i], b[i], c, 0, 0, 0);
@@ -129,20 +132,18 @@ __device__ __forceinline__ int fresh_thread() {
 }
 
 // a * (f[0] + f[1] + ...), the small parts first.
-template <typename T>
-__device__ __forceinline__ f32x4 mma_wide(typename Mat<T>::Frag a, const typename Mat<T>::Frag (&f)[Mat<T>::kWide],
-                                          f32x4 c) {
+template <typename T, int PARTS>
+__device__ __forceinline__ f32x4 mma_wide(typename Mat<T>::Frag a, const typename Mat<T>::Frag (&f)[PARTS], f32x4 c) {
 #pragma unroll
-    for (int i = Mat<T>::kWide - 1; i >= 0; i--) c = Mat<T>::mma(a, f[i], c);
+    for (int i = PARTS - 1; i >= 0; i--) c = Mat<T>::mma(a, f[i], c);
     return c;
 }
 
 // (f[0] + f[1] + ...) * b.
-template <typename T>
-__device__ __forceinline__ f32x4 wide_mma(const typename Mat<T>::Frag (&f)[Mat<T>::kWide], typename Mat<T>::Frag b,
-                                          f32x4 c) {
+template <typename T, int PARTS>
+__device__ __forceinline__ f32x4 wide_mma(const typename Mat<T>::Frag (&f)[PARTS], typename Mat<T>::Frag b, f32x4 c) {
 #pragma unroll
-    for (int i = Mat<T>::kWide - 1; i >= 0; i--) c = Mat<T>::mma(f[i], b, c);
+    for (int i = PARTS - 1; i >= 0; i--) c = Mat<T>::mma(f[i], b, c);
     return c;
 }
 

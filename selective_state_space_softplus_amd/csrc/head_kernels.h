@@ -269,8 +269,11 @@ __device__ __forceinline__ void state_write(const f32x4 (&acc)[JOBS][NP / 16], c
 }
 
 // acc = decay * acc + K^T (w V): K a tile [step][n], V the wave's columns of a
-// tile [step][channel], w the steps' weights.
-template <typename T, int NP, int JOBS>
+// tile [step][channel], w the steps' weights.  With bf16 inputs w V goes in as
+// PARTS bf16 operands: three where the state is an output, which makes it what
+// fp32 products would give (error against 64 bits 1e-7 relative); two where it
+// only feeds others (2e-6).
+template <typename T, int NP, int JOBS, int PARTS>
 __device__ __forceinline__ void state_update(f32x4 (&acc)[JOBS][NP / 16], float decay, const T* k_lds,
                                              const typename Mat<T>::Frag (&vf)[JOBS][2], const float* weights,
                                              int lane) {
@@ -295,7 +298,7 @@ __device__ __forceinline__ void state_update(f32x4 (&acc)[JOBS][NP / 16], float 
     for (int ct = 0; ct < JOBS; ct++)
 #pragma unroll
         for (int nt = 0; nt < NP / 16; nt++) acc[ct][nt] *= decay;
-    typename M::Frag w[JOBS][M::kWide];
+    typename M::Frag w[JOBS][PARTS];
 #pragma unroll
     for (int i = 0; i < kBatches; i++) {
         if (i + 1 < kBatches) load_k(i + 1);
@@ -305,9 +308,9 @@ __device__ __forceinline__ void state_update(f32x4 (&acc)[JOBS][NP / 16], float 
             const int at = 4 * i + k, kk = at / (NP / 16), nt = at % (NP / 16);
             if (nt == 0)
 #pragma unroll
-                for (int ct = 0; ct < JOBS; ct++) M::split(M::unpack(vf[ct][kk]) * wv[kk], w[ct]);
+                for (int ct = 0; ct < JOBS; ct++) M::template split<PARTS>(M::unpack(vf[ct][kk]) * wv[kk], w[ct]);
 #pragma unroll
-            for (int ct = 0; ct < JOBS; ct++) acc[ct][nt] = mma_wide<T>(kf[i & 1][k], w[ct], acc[ct][nt]);
+            for (int ct = 0; ct < JOBS; ct++) acc[ct][nt] = mma_wide<T, PARTS>(kf[i & 1][k], w[ct], acc[ct][nt]);
         }
     }
 }
@@ -321,7 +324,7 @@ enum class StateMode { Local, Chunks };
 //   Chunks: from seg_state (several segments) or the given end state; the state
 //           at entry to every chunk goes to chunk_s or chunk_q, the adjoint one
 //           past the sequence's start to dh0.
-template <typename T, int NP, int JOBS, bool REV, StateMode MODE>
+template <typename T, int NP, int JOBS, int PARTS, bool REV, StateMode MODE>
 __global__ __launch_bounds__(256, 2) void head_states(HeadParams p) {
     using M = Mat<T>;
     using TileK = Tile<T, NP>;
@@ -405,7 +408,7 @@ __global__ __launch_bounds__(256, 2) void head_states(HeadParams p) {
         const GateLds& gt = gates[w.job];
         const float cq = gt.c[63].x;
         total += cq;
-        state_update<T, NP, JOBS>(acc, exp2_hw(cq), k_lds, vf, REV ? gt.in : gt.out, lane);
+        state_update<T, NP, JOBS, PARTS>(acc, exp2_hw(cq), k_lds, vf, REV ? gt.in : gt.out, lane);
         if (done) it++;
     }
     if (!w.my_alive) return;
@@ -448,7 +451,7 @@ __global__ __launch_bounds__(256) void head_carry(HeadParams p) {
 // the state, held as the accumulators of the update, is rounded to bf16 in
 // place as the second operand of the readout (its rows n are the product's k:
 // lane group g holds n = 4 g + 0..3 of two 16-row tiles).
-template <typename T, int NP, int JOBS>
+template <typename T, int NP, int JOBS, int PARTS>
 __global__ __launch_bounds__(256, 2) void head_out(HeadParams p) {
     using M = Mat<T>;
     using TileK = Tile<T, NP>;
@@ -661,7 +664,7 @@ __global__ __launch_bounds__(256, 2) void head_out(HeadParams p) {
 #pragma unroll
             for (int it = 0; it < 4; it++) store4(at + 16 * it * TileV::kLd, out[ct][it] + skip * xd[it]);
         }
-        state_update<T, NP, JOBS>(acc, exp2_hw(gt.c[63].x), b_lds, xf, gt.out, lane);
+        state_update<T, NP, JOBS, PARTS>(acc, exp2_hw(gt.c[63].x), b_lds, xf, gt.out, lane);
         if (done) ck++;
     }
     barrier_lds();
@@ -682,9 +685,10 @@ __global__ __launch_bounds__(256, 2) void head_out(HeadParams p) {
 //     dlog_t = sum_{i >= t > j} W_ij + sum_{i >= t} Y_i + sum_{j < t} X_j + exp(c_63) <Q, S>
 // The first sum is that over i >= t of the rows' sums less the columns' sums of
 // W below its diagonal (the diagonal, where W is largest, would only cancel).
-// These feed fp32 outputs, so their products keep S and Q as three bf16 parts;
-// R, the scores and the Q of dx, which only feed outputs of the inputs' type,
-// are rounded.
+// These feed fp32 outputs, so their products keep S and Q as two bf16 parts
+// (2^-18 of an element at most, and independent between elements); R, the
+// scores and the Q of dx, which only feed outputs of the inputs' type, are
+// rounded.
 //
 // A workgroup of 8 waves takes one chunk and the heads of its block in turn.
 // The scores' 64 x 64 tile goes to the waves by two 16 x 16 pieces, dB and dC
@@ -722,7 +726,7 @@ __global__ __launch_bounds__(512, 2) void head_grad(HeadParams p) {
     using TileK = Tile<T, NP, 512>;
     using TileV = Tile<T, kHeadSlab, 512>;
     constexpr int NT = NP / 16, ITW = NP / 32;   // tiles of n; row tiles of a wave's share of dB and dC
-    constexpr int kLdK = TileK::kLd, kLdV = TileV::kLd;
+    constexpr int kLdK = TileK::kLd, kLdV = TileV::kLd, PARTS = sizeof(T) == 2 ? 2 : 1;
     extern __shared__ __align__(16) float smem[];
     GradLds<T, NP>& lds = *reinterpret_cast<GradLds<T, NP>*>(smem);
 
@@ -784,6 +788,13 @@ __global__ __launch_bounds__(512, 2) void head_grad(HeadParams p) {
     };
     fetch(h_first, 0);
     fetch_states(h_first, 0);
+    // What lies above the diagonal is written once.
+    for (int i = threadIdx.x; i < Tile<T, kHeadSlab>::kElems; i += 512) lds.m[i] = lds.r[i] = T(0);
+    for (int k = 0; k < 2; k++) {
+        for (int i = threadIdx.x; i < 16 * 64; i += 512) lds.shares[k].col[i / 64][i % 64] = 0.0f;
+        if (threadIdx.x < 128) lds.shares[k].row[threadIdx.x / 64][threadIdx.x % 64] = 0.0f;
+        if (threadIdx.x < 8) lds.shares[k].dsum[threadIdx.x] = 0.0f;
+    }
     barrier_lds();
 
     f32x4 cb[2];   // C_i . B_j, rows i = 16 si + 4 lg + r, columns j = 16 (sj + k) + lr
@@ -884,10 +895,11 @@ __global__ __launch_bounds__(512, 2) void head_grad(HeadParams p) {
             }
             const float* const ci = reinterpret_cast<const float*>(gates.c + 16 * si + 4 * lg);
             const f32x4 c01 = floats4(ci), c23 = floats4(ci + 4);
-            f32x2 cj[2];
+            f32x2 cj[2], ce[2];
             float sj_[2];
 #pragma unroll
             for (int k = 0; k < 2; k++) {
+                ce[k] = gates.c[16 * (sj + k) + 15];
                 cj[k] = gates.c[16 * (sj + k) + lr];
                 sj_[k] = gates.step[16 * (sj + k) + lr];
             }
@@ -897,52 +909,65 @@ __global__ __launch_bounds__(512, 2) void head_grad(HeadParams p) {
 #pragma unroll
             for (int k = 0; k < 2; k++) {
                 const int jt = sj + k, j = 16 * jt + lr;
-                f32x4 gs = {0, 0, 0, 0}, ms, rs;
+                if (jt > si) break;   // above the diagonal: zeros from the start
+                f32x4 gs = {0, 0, 0, 0}, w, ms, rs;
 #pragma unroll
                 for (int kk = 0; kk < 2; kk++) gs = M::mma(yf[kk], xf[k][kk], gs);
-                float col = 0.0f, on = 0.0f;
+                // exp(c_i - c_j); below the diagonal tile by way of the last step of tile jt.
+                const f32x2 by = jt < si ? ce[k] : cj[k];
 #pragma unroll
                 for (int r = 0; r < 4; r++) {
-                    const int i = 16 * si + 4 * lg + r;
                     const f32x4 cc = r < 2 ? c01 : c23;
-                    const float e = exp2_hw(c_diff(f32x2{cc[2 * (r & 1)], cc[2 * (r & 1) + 1]}, cj[k]));
-                    const float w = j <= i ? e : 0.0f;
-                    ms[r] = j <= i ? w * cb[k][r] : 0.0f;
-                    rs[r] = j <= i ? w * gs[r] * sj_[k] : 0.0f;
-                    const float pr = ms[r] * gs[r];
-                    const float below = j < i ? pr : 0.0f;
-                    col += below;
-                    row_sum[r] += below * sj_[k];
-                    on = j == i ? pr : on;
-                    diag += j == i ? gs[r] : 0.0f;
+                    w[r] = exp2_hw(c_diff(f32x2{cc[2 * (r & 1)], cc[2 * (r & 1) + 1]}, by));
                 }
+                f32x4 below;
+                if (jt < si) {
+                    w *= exp2_hw(c_diff(ce[k], cj[k]));
+                    ms = w * cb[k];
+                    rs = w * gs * sj_[k];
+                    below = ms * gs;
+                } else {
+                    float on = 0.0f;
+#pragma unroll
+                    for (int r = 0; r < 4; r++) {
+                        const int i = 4 * lg + r;   // in the tile
+                        ms[r] = lr <= i ? w[r] * cb[k][r] : 0.0f;
+                        rs[r] = lr <= i ? w[r] * gs[r] * sj_[k] : 0.0f;
+                        below[r] = lr < i ? ms[r] * gs[r] : 0.0f;
+                        on = lr == i ? ms[r] * gs[r] : on;
+                        diag = lr == i ? gs[r] : diag;
+                    }
+                    if (lr / 4 == lg) shares.diag[j] = on;
+                }
+                row_sum += below * sj_[k];
                 store4(lds.m + j * kLdV + 16 * si + 4 * lg, ms);
                 store4(lds.r + j * kLdV + 16 * si + 4 * lg, rs);
-                shares.col[4 * si + lg][j] = col;
-                if (jt == si && lr / 4 == lg) shares.diag[j] = on;
+                shares.col[4 * si + lg][j] = (below[0] + below[1]) + (below[2] + below[3]);
             }
+            if (sj <= si) {
 #pragma unroll
-            for (int r = 0; r < 4; r++) {
-                const float v = sum_lanes16(row_sum[r]);
-                if (lr == 0) shares.row[wave & 1][16 * si + 4 * lg + r] = v;
+                for (int r = 0; r < 4; r++) {
+                    const float v = sum_lanes16(row_sum[r]);
+                    if (lr == 0) shares.row[wave & 1][16 * si + 4 * lg + r] = v;
+                }
+                diag = running_sum(diag);
+                if (lane == 63) shares.dsum[wave] = diag;
             }
-            diag = sum_wave(diag);
-            if (lane == 0) shares.dsum[wave] = diag;
         }
         // S and Q as operands; Q rounded for dx, by the waves that hold it first.
-        typename M::Frag sf[2][M::kWide], qf[2][M::kWide];
+        typename M::Frag sf[2][PARTS], qf[2][PARTS];
         float dot = 0.0f;
 #pragma unroll
         for (int kk = 0; kk < 2; kk++) {
-            M::split(sv[kk], sf[kk]);
-            M::split(qv[kk], qf[kk]);
+            M::template split<PARTS>(sv[kk], sf[kk]);
+            M::template split<PARTS>(qv[kk], qf[kk]);
 #pragma unroll
             for (int e = 0; e < 8; e++) dot += sv[kk][e] * qv[kk][e];
             if constexpr (sizeof(T) == 2)
                 if (it0 == 0) *reinterpret_cast<typename M::Frag*>(lds.q + n * kLdV + 32 * kk + 8 * lg) = qf[kk][0];
         }
-        dot = sum_wave(dot);
-        if (lane == 0 && it0 == 0) shares.dot[nt] = dot;
+        dot = running_sum(dot);
+        if (lane == 63 && it0 == 0) shares.dot[nt] = dot;
         if (next_h < h_last) fetch_states(next_h, next_slab);
         barrier_lds();
 
@@ -965,8 +990,8 @@ __global__ __launch_bounds__(512, 2) void head_grad(HeadParams p) {
             f32x4 u = {0, 0, 0, 0}, v = {0, 0, 0, 0};   // rows n = 16 nt + 4 lg + r of column i0 + lr
 #pragma unroll
             for (int kk = 0; kk < 2; kk++) {
-                u = wide_mma<T>(sf[kk], yf[kk], u);
-                v = wide_mma<T>(qf[kk], xf[kk], v);
+                u = wide_mma<T, PARTS>(sf[kk], yf[kk], u);
+                v = wide_mma<T, PARTS>(qf[kk], xf[kk], v);
             }
             const f32x4 uc = u * cv, vb = v * bv;
             const float sums = sum_groups4_pair(((uc[0] + uc[1]) + (uc[2] + uc[3])) * in,
@@ -975,11 +1000,11 @@ __global__ __launch_bounds__(512, 2) void head_grad(HeadParams p) {
             if (lg == 2) shares.xin[nt][i0 + lr] = sums;
             dc[k] += u * in;
             db[k] += v * out;
-#pragma unroll
-            for (int kk = 0; kk < 2; kk++) {
-                dc[k] = M::mma(bf[kk], rc[kk], dc[k]);
-                db[k] = M::mma(cf[kk], rr[kk], db[k]);
-            }
+            // R's zeros: steps j of the second half do not reach rows of the first, nor those rows the second's columns.
+            dc[k] = M::mma(bf[0], rc[0], dc[k]);
+            if (it0 + k >= 2) dc[k] = M::mma(bf[1], rc[1], dc[k]);
+            if (it0 + k < 2) db[k] = M::mma(cf[0], rr[0], db[k]);
+            db[k] = M::mma(cf[1], rr[1], db[k]);
         }
 
         // dx.

@@ -63,10 +63,11 @@ int64_t segments(const Shape& s, int dtype) {
 }
 
 // Heads of a group whose shares of dB and dC one workgroup of the backward
-// adds up: all of them, unless that leaves fewer than 1024 workgroups.
+// adds up: all of them, unless that leaves compute units without a workgroup (256, one
+// workgroup each: b = 8, L = 2048, H = 24, G = 1 takes 182 us with one block, 204 + 22 for adding four up).
 int64_t heads_per_block(const Shape& s) {
     const int64_t base = s.b * s.chunks() * s.G, per_group = s.H / s.G;
-    const int64_t blocks = std::max<int64_t>(1, std::min((1024 + base - 1) / base, per_group));
+    const int64_t blocks = std::max<int64_t>(1, std::min((256 + base - 1) / base, per_group));
     return (per_group + blocks - 1) / blocks;
 }
 
@@ -153,17 +154,29 @@ unsigned walkers(const HeadParams& p, int jobs, int nseg) {
 
 // The states at the segments' starts (REV: the adjoint states at their ends).  The last segment of the walk needs
 // no pass of its own.
-template <typename T, int NP, int JOBS, bool REV>
+template <typename T, int NP, int JOBS, int PARTS, bool REV>
 void carry_segments(const HeadParams& p, hipStream_t st) {
-    ss::head_states<T, NP, JOBS, REV, StateMode::Local>
+    ss::head_states<T, NP, JOBS, PARTS, REV, StateMode::Local>
         <<<walkers(p, JOBS, p.nseg - 1), 256, ss::head_states_lds<T, NP, JOBS>(), st>>>(p);
     ss::head_carry<NP, REV><<<unsigned(p.b * p.H * p.slabs) * (NP * 64 / 256), 256, 0, st>>>(p);
 }
 
+// Parts of the weighted operand of the states' products (fp32 has it whole): three where the states are an output.
+template <typename T, typename F>
+void by_parts(bool exact, F&& f) {
+    if constexpr (sizeof(T) == 4) f(std::integral_constant<int, 1>{});
+    else if (exact) f(std::integral_constant<int, 3>{});
+    else f(std::integral_constant<int, 2>{});
+}
+
 template <typename T, int NP, int JOBS>
 int run_fwd(const HeadParams& p, hipStream_t st) {
-    if (p.nseg > 1) carry_segments<T, NP, JOBS, false>(p, st);
-    ss::head_out<T, NP, JOBS><<<walkers(p, JOBS, p.nseg), 256, ss::head_out_lds<T, NP, JOBS>(), st>>>(p);
+    by_parts<T>(p.last != nullptr, [&](auto parts) {
+        constexpr int PARTS = decltype(parts)::value;
+        if (p.nseg > 1) carry_segments<T, NP, JOBS, PARTS, false>(p, st);
+        ss::head_out<T, NP, JOBS, PARTS>
+            <<<walkers(p, JOBS, p.nseg), 256, ss::head_out_lds<T, NP, JOBS>(), st>>>(p);
+    });
     return status(hipGetLastError());
 }
 
@@ -171,10 +184,16 @@ template <typename T, int NP, int JOBS>
 int run_bwd(HeadParams p, hipStream_t st) {
     static_assert(ss::head_grad_lds<T, NP>() <= 160 * 1024, "LDS of a compute unit");
     constexpr size_t lds = ss::head_states_lds<T, NP, JOBS>();
-    if (p.nseg > 1) carry_segments<T, NP, JOBS, false>(p, st);
-    ss::head_states<T, NP, JOBS, false, StateMode::Chunks><<<walkers(p, JOBS, p.nseg), 256, lds, st>>>(p);
-    if (p.nseg > 1) carry_segments<T, NP, JOBS, true>(p, st);
-    ss::head_states<T, NP, JOBS, true, StateMode::Chunks><<<walkers(p, JOBS, p.nseg), 256, lds, st>>>(p);
+    by_parts<T>(false, [&](auto parts) {
+        constexpr int PARTS = decltype(parts)::value;
+        if (p.nseg > 1) carry_segments<T, NP, JOBS, PARTS, false>(p, st);
+        ss::head_states<T, NP, JOBS, PARTS, false, StateMode::Chunks><<<walkers(p, JOBS, p.nseg), 256, lds, st>>>(p);
+    });
+    by_parts<T>(p.dh0 != nullptr, [&](auto parts) {
+        constexpr int PARTS = decltype(parts)::value;
+        if (p.nseg > 1) carry_segments<T, NP, JOBS, PARTS, true>(p, st);
+        ss::head_states<T, NP, JOBS, PARTS, true, StateMode::Chunks><<<walkers(p, JOBS, p.nseg), 256, lds, st>>>(p);
+    });
     const unsigned grid = unsigned(p.b * p.chunks * p.G * p.blocks);
     ss::head_grad<T, NP><<<grid, 512, ss::head_grad_lds<T, NP>(), st>>>(p);
     if (p.blocks > 1) {
