@@ -26,7 +26,7 @@ import ctypes
 
 import torch
 
-from . import SS_BF16, SS_F32, SSError, _check, _dtype_code, _ptr, _stream, _workspace, lib
+from . import SS_BF16, SS_F32, SSError, _check as _check_slow, lib
 
 SS_MAX_HEAD_STATE = 128
 SS_MAX_HEAD_DIM = 1024
@@ -53,6 +53,61 @@ _SIGNATURES = {
 for _name, (_res, _args) in _SIGNATURES.items():
     getattr(lib, _name).restype = _res
     getattr(lib, _name).argtypes = _args
+
+
+_CODES = {torch.float32: SS_F32, torch.bfloat16: SS_BF16}
+
+
+def _dtype_code(dtype):
+    code = _CODES.get(dtype)
+    if code is None:
+        raise TypeError(f"inputs must be float32 or bfloat16, got {dtype}")
+    return code
+
+
+def _check(t, name, shape, dtype, device):
+    """The package's check of a contiguous tensor; one that passes costs a few comparisons (a decode step is small)."""
+    if t is not None and not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+                              and t.device == device and t.is_contiguous()):
+        _check_slow(t, name, shape, dtype, device)
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _raw_stream(index):
+    return torch._C._cuda_getCurrentRawStream(index)
+
+
+def _call(fn, where, device, *args):
+    """fn(*args, stream) on the current stream of `device`, which is made the current device if it is not."""
+    index = device.index
+    if index == torch.cuda.current_device():
+        rc = fn(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, _raw_stream(index))
+    if rc != 0:
+        raise SSError(rc, where)
+
+
+_workspaces: dict = {}
+
+
+def _workspace(device, nbytes: int):
+    """A uint8 device buffer of at least nbytes, cached for this device and its current stream; under graph capture one
+    of the graph's own, which later growth of the cached one does not free."""
+    if nbytes == 0:
+        return None
+    if torch.cuda.is_current_stream_capturing():
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    key = (device.index, _raw_stream(device.index))
+    ws = _workspaces.get(key)
+    if ws is None or ws.numel() < nbytes:
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        _workspaces[key] = ws
+    return ws
 
 
 def _check_tokens(t, name, shape, dtype, device):
@@ -120,12 +175,9 @@ def head_scan_fwd(x, delta, A_log, B, C, D, delta_bias=None, delta_softplus=True
         return (y, last_state) if return_last_state else y
     if workspace is None:
         workspace = _workspace(dev, int(lib.ss_head_scan_fwd_workspace_bytes(b, L, H, P, N, G, code)))
-    with torch.cuda.device(dev):
-        rc = lib.ss_head_scan_fwd(_ptr(x), _ptr(delta), _ptr(A_log), _ptr(B), _ptr(C), _ptr(D), _ptr(delta_bias),
-                                  int(bool(delta_softplus)), _ptr(initial_state), _ptr(y), _ptr(last_state),
-                                  b, L, H, P, N, G, code, strides, _ptr(workspace), _bytes(workspace), _stream(dev))
-    if rc != 0:
-        raise SSError(rc, "ss_head_scan_fwd")
+    _call(lib.ss_head_scan_fwd, "ss_head_scan_fwd", dev, _ptr(x), _ptr(delta), _ptr(A_log), _ptr(B),
+          _ptr(C), _ptr(D), _ptr(delta_bias), int(bool(delta_softplus)), _ptr(initial_state), _ptr(y),
+          _ptr(last_state), b, L, H, P, N, G, code, strides, _ptr(workspace), _bytes(workspace))
     return (y, last_state) if return_last_state else y
 
 
@@ -158,14 +210,11 @@ def head_scan_bwd(x, delta, A_log, B, C, D, dy, delta_bias=None, delta_softplus=
         # Several times the size of the inputs: a buffer of its own, not kept.
         workspace = torch.empty(int(lib.ss_head_scan_bwd_workspace_bytes(b, L, H, P, N, G, code)), dtype=torch.uint8,
                                 device=dev)
-    with torch.cuda.device(dev):
-        rc = lib.ss_head_scan_bwd(_ptr(x), _ptr(delta), _ptr(A_log), _ptr(B), _ptr(C), _ptr(D), _ptr(delta_bias),
-                                  int(bool(delta_softplus)), _ptr(initial_state), _ptr(dy), _ptr(dlast_state),
-                                  _ptr(g["dx"]), _ptr(g["ddelta"]), _ptr(g["dA_log"]), _ptr(g["dB"]), _ptr(g["dC"]),
-                                  _ptr(g["dD"]), _ptr(g.get("ddelta_bias")), _ptr(g.get("dinitial_state")),
-                                  b, L, H, P, N, G, code, strides, _ptr(workspace), _bytes(workspace), _stream(dev))
-    if rc != 0:
-        raise SSError(rc, "ss_head_scan_bwd")
+    _call(lib.ss_head_scan_bwd, "ss_head_scan_bwd", dev, _ptr(x), _ptr(delta), _ptr(A_log), _ptr(B),
+          _ptr(C), _ptr(D), _ptr(delta_bias), int(bool(delta_softplus)), _ptr(initial_state), _ptr(dy),
+          _ptr(dlast_state), _ptr(g["dx"]), _ptr(g["ddelta"]), _ptr(g["dA_log"]), _ptr(g["dB"]), _ptr(g["dC"]),
+          _ptr(g["dD"]), _ptr(g.get("ddelta_bias")), _ptr(g.get("dinitial_state")), b, L, H, P, N, G, code,
+          strides, _ptr(workspace), _bytes(workspace))
     return g
 
 
@@ -217,12 +266,9 @@ def head_state_update(state, x, dt, A_log, B, C, D, dt_bias=None, dt_softplus=Tr
         if y.numel():
             y.copy_(x * D[:, None])
         return y
-    with torch.cuda.device(dev):
-        rc = lib.ss_head_state_update(_ptr(state), _ptr(x), _ptr(dt), _ptr(A_log), _ptr(B), _ptr(C), _ptr(D),
-                                      _ptr(dt_bias), int(bool(dt_softplus)), _ptr(y), b, H, P, N, G, code,
-                                      _stream(dev))
-    if rc != 0:
-        raise SSError(rc, "ss_head_state_update")
+    _call(lib.ss_head_state_update, "ss_head_state_update", dev, _ptr(state), _ptr(x), _ptr(dt),
+          _ptr(A_log), _ptr(B), _ptr(C), _ptr(D), _ptr(dt_bias), int(bool(dt_softplus)), _ptr(y), b, H, P, N, G,
+          code)
     return y
 
 
@@ -285,12 +331,8 @@ def residual_norm_fwd(x, weight, residual=None, scale=None, eps=1e-5, residual_d
     _check(residual_out, "residual_out", x.shape, rt, dev)
     if rows == 0 or d == 0:
         return out, residual_out
-    with torch.cuda.device(dev):
-        rc = lib.ss_residual_norm_fwd(_ptr(x), _ptr(residual), _ptr(scale), _ptr(weight), _ptr(out),
-                                      _ptr(residual_out), rows, d, float(eps), code, _dtype_code(rt), x_stride,
-                                      _stream(dev))
-    if rc != 0:
-        raise SSError(rc, "ss_residual_norm_fwd")
+    _call(lib.ss_residual_norm_fwd, "ss_residual_norm_fwd", dev, _ptr(x), _ptr(residual), _ptr(scale),
+          _ptr(weight), _ptr(out), _ptr(residual_out), rows, d, float(eps), code, _dtype_code(rt), x_stride)
     return out, residual_out
 
 
@@ -327,14 +369,10 @@ def residual_norm_bwd(dout, residual_out, weight, dresidual_out=None, x=None, sc
     else:
         if workspace is None:
             workspace = _workspace(dev, int(lib.ss_residual_norm_bwd_workspace_bytes(rows, d)))
-        with torch.cuda.device(dev):
-            rc = lib.ss_residual_norm_bwd(_ptr(dout), _ptr(dresidual_out), _ptr(residual_out),
-                                          _ptr(x) if scale is not None else None, _ptr(scale), _ptr(weight),
-                                          _ptr(g["dx"]), _ptr(g.get("dresidual")), _ptr(g["dweight"]),
-                                          _ptr(g.get("dscale")), rows, d, float(eps), code, _dtype_code(rt), x_stride,
-                                          _ptr(workspace), _bytes(workspace), _stream(dev))
-        if rc != 0:
-            raise SSError(rc, "ss_residual_norm_bwd")
+        _call(lib.ss_residual_norm_bwd, "ss_residual_norm_bwd", dev, _ptr(dout), _ptr(dresidual_out),
+              _ptr(residual_out), _ptr(x) if scale is not None else None, _ptr(scale), _ptr(weight),
+              _ptr(g["dx"]), _ptr(g.get("dresidual")), _ptr(g["dweight"]), _ptr(g.get("dscale")), rows, d,
+              float(eps), code, _dtype_code(rt), x_stride, _ptr(workspace), _bytes(workspace))
     if need_dresidual and not apart:
         g["dresidual"] = g["dx"]
     return g
@@ -375,11 +413,8 @@ def gated_norm_fwd(y, z, weight, groups=1, eps=1e-5, norm_before_gate=False, out
     _check(out, "out", y.shape, y.dtype, dev)
     if rows == 0 or d == 0:
         return out
-    with torch.cuda.device(dev):
-        rc = lib.ss_gated_norm_fwd(_ptr(y), _ptr(z), _ptr(weight), _ptr(out), rows, d, int(groups), float(eps),
-                                   int(bool(norm_before_gate)), code, y_stride, z_stride, _stream(dev))
-    if rc != 0:
-        raise SSError(rc, "ss_gated_norm_fwd")
+    _call(lib.ss_gated_norm_fwd, "ss_gated_norm_fwd", dev, _ptr(y), _ptr(z), _ptr(weight), _ptr(out), rows,
+          d, int(groups), float(eps), int(bool(norm_before_gate)), code, y_stride, z_stride)
     return out
 
 
@@ -400,12 +435,9 @@ def gated_norm_bwd(dout, y, z, weight, groups=1, eps=1e-5, norm_before_gate=Fals
         return g
     if workspace is None:
         workspace = _workspace(dev, int(lib.ss_gated_norm_bwd_workspace_bytes(rows, d, int(groups))))
-    with torch.cuda.device(dev):
-        rc = lib.ss_gated_norm_bwd(_ptr(dout), _ptr(y), _ptr(z), _ptr(weight), _ptr(g["dy"]), _ptr(g["dz"]),
-                                   _ptr(g["dweight"]), rows, d, int(groups), float(eps), int(bool(norm_before_gate)),
-                                   code, y_stride, z_stride, _ptr(workspace), _bytes(workspace), _stream(dev))
-    if rc != 0:
-        raise SSError(rc, "ss_gated_norm_bwd")
+    _call(lib.ss_gated_norm_bwd, "ss_gated_norm_bwd", dev, _ptr(dout), _ptr(y), _ptr(z), _ptr(weight),
+          _ptr(g["dy"]), _ptr(g["dz"]), _ptr(g["dweight"]), rows, d, int(groups), float(eps),
+          int(bool(norm_before_gate)), code, y_stride, z_stride, _ptr(workspace), _bytes(workspace))
     return g
 
 

@@ -1101,44 +1101,71 @@ __global__ __launch_bounds__(256) void head_sum_chunks(HeadParams p) {
     if (threadIdx.x == 0 && out) out[h] = (part[0] + part[1]) + (part[2] + part[3]);
 }
 
-// One decode step.  A row (b, h, p) of the state is N consecutive values:
-// LPR lanes take 4 of them at a time (VEC) or one, and share the readout's sum.
-template <typename T, int LPR, bool VEC>
+// One decode step, bound by the state's one read and one write.  A row (b, h, p)
+// of the state is N consecutive values, taken by LPR lanes of 4 (VEC) or one
+// each; a workgroup takes up to ROWS rows a lane group of one head, all their
+// loads under way together, so that B, C and the decay are formed once.
+template <typename T, int LPR, int ROWS, bool VEC>
 __global__ __launch_bounds__(256) void head_step(float* state, const T* x, const T* dt, const float* A_log, const T* B,
                                                  const T* C, const float* D, const float* dt_bias, int use_softplus,
-                                                 T* y, int64_t b, int H, int P, int N, int G) {
-    const int64_t row = (int64_t(blockIdx.x) * 256 + threadIdx.x) / LPR, rows = b * H * P;
-    const int sub = threadIdx.x % LPR;
-    if (row >= rows) return;   // whole groups of LPR lanes leave together
-    const int64_t bh = row / P, bi = bh / H;
-    const int h = int(bh % H);
+                                                 T* y, int H, int P, int N, int G, int blocks) {
+    constexpr int V = VEC ? 4 : 1, GROUPS = 256 / LPR;
+    const int64_t bh = blockIdx.x / unsigned(blocks), bi = bh / H;
+    const int h = int(bh % H), sub = int(threadIdx.x) % LPR;
+    const int p0 = int(blockIdx.x % unsigned(blocks)) * GROUPS * ROWS + int(threadIdx.x) / LPR;
     const int64_t bg = (bi * G + h / (H / G)) * N;
+    float* const s = state + bh * P * N;
+    float sum[ROWS], xv[ROWS];
+#pragma unroll
+    for (int k = 0; k < ROWS; k++) {
+        const int p = p0 + k * GROUPS;
+        sum[k] = 0.0f;
+        xv[k] = p < P ? Elem<T>::load(x, bh * P + p) : 0.0f;
+    }
     const float step = step_size(Elem<T>::load(dt, bh), dt_bias ? dt_bias[h] : 0.0f, use_softplus);
     const float a = exp2_hw(step * a2_from_alog(A_log[h]));
-    const float xv = Elem<T>::load(x, row), sx = step * xv;
-    float* const s = state + row * N;
-    float sum = 0.0f;
-    constexpr int V = VEC ? 4 : 1;
     for (int n = sub * V; n < N; n += LPR * V) {
-        float v[V];
-        if constexpr (VEC) {
-            const f32x4 w = *reinterpret_cast<const f32x4*>(s + n);
+        float v[ROWS][V], bv[V], cv[V];
 #pragma unroll
-            for (int e = 0; e < V; e++) v[e] = w[e];
-        } else {
-            v[0] = s[n];
+        for (int k = 0; k < ROWS; k++) {
+            const int p = p0 + k * GROUPS;
+            if (p < P) {
+                if constexpr (VEC) {
+                    const f32x4 w = *reinterpret_cast<const f32x4*>(s + int64_t(p) * N + n);
+#pragma unroll
+                    for (int e = 0; e < V; e++) v[k][e] = w[e];
+                } else {
+                    v[k][0] = s[int64_t(p) * N + n];
+                }
+            }
         }
 #pragma unroll
         for (int e = 0; e < V; e++) {
-            v[e] = a * v[e] + sx * Elem<T>::load(B, bg + n + e);
-            sum += v[e] * Elem<T>::load(C, bg + n + e);
+            bv[e] = Elem<T>::load(B, bg + n + e) * step;
+            cv[e] = Elem<T>::load(C, bg + n + e);
         }
-        if constexpr (VEC) *reinterpret_cast<f32x4*>(s + n) = f32x4{v[0], v[1], v[2], v[3]};
-        else s[n] = v[0];
+#pragma unroll
+        for (int k = 0; k < ROWS; k++) {
+            const int p = p0 + k * GROUPS;
+            if (p < P) {
+#pragma unroll
+                for (int e = 0; e < V; e++) {
+                    v[k][e] = a * v[k][e] + xv[k] * bv[e];
+                    sum[k] += v[k][e] * cv[e];
+                }
+                if constexpr (VEC)
+                    *reinterpret_cast<f32x4*>(s + int64_t(p) * N + n) = f32x4{v[k][0], v[k][1], v[k][2], v[k][3]};
+                else s[int64_t(p) * N + n] = v[k][0];
+            }
+        }
     }
 #pragma unroll
-    for (int m = 1; m < LPR; m <<= 1) sum += __shfl_xor(sum, m);
-    if (sub == 0) Elem<T>::store(y, row, sum + D[h] * xv);
+    for (int k = 0; k < ROWS; k++) {
+#pragma unroll
+        for (int m = 1; m < LPR; m <<= 1) sum[k] += __shfl_xor(sum[k], m);
+        const int p = p0 + k * GROUPS;
+        if (sub == 0 && p < P) Elem<T>::store(y, bh * P + p, sum[k] + D[h] * xv[k]);
+    }
 }
 
 // LDS bytes of the kernels above.

@@ -232,18 +232,24 @@ int dispatch_bwd(const HeadParams& p, hipStream_t st) {
     return padded_state(p.N, true) == 64 ? bwd_jobs<T, 64>(p, st) : bwd_jobs<T, 128>(p, st);
 }
 
-template <typename T, bool VEC>
-void launch_step(int lpr, int64_t rows, hipStream_t st, float* state, const T* x, const T* dt, const float* A_log,
-                 const T* B, const T* C, const float* D, const float* bias, int softplus, T* y, int64_t b, int H,
-                 int P, int N, int G) {
-    auto run = [&](auto kernel, int lanes) {
-        kernel<<<unsigned((rows * lanes + 255) / 256), 256, 0, st>>>(state, x, dt, A_log, B, C, D, bias, softplus, y, b,
-                                                                     H, P, N, G);
+template <typename T, int LPR, bool VEC>
+void launch_step(float* state, const void* x, const void* dt, const float* A_log, const void* B, const void* C,
+                 const float* D, const float* bias, int softplus, void* y, const Shape& s, hipStream_t st) {
+    constexpr int groups = 256 / LPR;
+    auto run = [&](auto rows) {
+        constexpr int ROWS = decltype(rows)::value;
+        const int64_t blocks = (s.P + groups * ROWS - 1) / (groups * ROWS);
+        ss::head_step<T, LPR, ROWS, VEC><<<unsigned(s.b * s.H * blocks), 256, 0, st>>>(
+            state, static_cast<const T*>(x), static_cast<const T*>(dt), A_log, static_cast<const T*>(B),
+            static_cast<const T*>(C), D, bias, softplus, static_cast<T*>(y), int(s.H), int(s.P), int(s.N), int(s.G),
+            int(blocks));
     };
-    if (lpr <= 4) run(ss::head_step<T, 4, VEC>, 4);
-    else if (lpr <= 8) run(ss::head_step<T, 8, VEC>, 8);
-    else if (lpr <= 16) run(ss::head_step<T, 16, VEC>, 16);
-    else run(ss::head_step<T, 32, VEC>, 32);
+    // Rows a lane group: 8 where that leaves a workgroup for every compute unit, one where there are few rows
+    // (b = 1, H = 24, P = 64, N = 128: 24 workgroups of 8 rows against 192 of one).
+    if (s.P > groups && s.b * s.H * ((s.P + groups * 8 - 1) / (groups * 8)) >= 256)
+        run(std::integral_constant<int, 8>{});
+    else
+        run(std::integral_constant<int, 1>{});
 }
 
 template <typename T>
@@ -252,14 +258,15 @@ int run_step(float* state, const void* x, const void* dt, const float* A_log, co
     // Lanes that cover a row of the state once, 16 bytes each where the rows allow it.
     const bool vec = s.N % 4 == 0 && aligned(state, 16);
     const int lpr = int(vec ? s.N / 4 : s.N);
-    auto go = [&](auto v) {
-        launch_step<T, decltype(v)::value>(lpr, s.b * s.H * s.P, st, state, static_cast<const T*>(x),
-                                           static_cast<const T*>(dt), A_log, static_cast<const T*>(B),
-                                           static_cast<const T*>(C), D, bias, softplus, static_cast<T*>(y), s.b,
-                                           int(s.H), int(s.P), int(s.N), int(s.G));
+    auto go = [&](auto lanes) {
+        constexpr int LPR = decltype(lanes)::value;
+        if (vec) launch_step<T, LPR, true>(state, x, dt, A_log, B, C, D, bias, softplus, y, s, st);
+        else launch_step<T, LPR, false>(state, x, dt, A_log, B, C, D, bias, softplus, y, s, st);
     };
-    if (vec) go(std::true_type{});
-    else go(std::false_type{});
+    if (lpr <= 4) go(std::integral_constant<int, 4>{});
+    else if (lpr <= 8) go(std::integral_constant<int, 8>{});
+    else if (lpr <= 16) go(std::integral_constant<int, 16>{});
+    else go(std::integral_constant<int, 32>{});
     return status(hipGetLastError());
 }
 

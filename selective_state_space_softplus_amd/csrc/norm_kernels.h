@@ -5,9 +5,10 @@
 // with inv = 1 / sqrt(mean(v^2) + eps) over a row (or a group of its channels).
 //
 // All of them move each element once and are bound by that: a row lives in
-// registers between its reduction and its outputs.  THREADS threads take a row
-// (64: a wave, four rows to a workgroup; 256 or 1024: the workgroup), each of
-// them VPT vectors of 8 channels.  Sums are fp32.
+// registers between its reduction and its outputs.  A row is a wave's (WAVE,
+// four rows to a workgroup) or a workgroup's, which has as many waves as the
+// row has 512-channel pieces, so that no lane is idle for long; a thread takes
+// VPT vectors of 8 channels.  Sums are fp32.
 //
 // Backward, with e = w * dout (times silu(z) where the norm is before the gate):
 //     dv = inv * (e - v * inv^2 * mean(e v))
@@ -41,6 +42,22 @@ __device__ __forceinline__ f32x8 load8(const float* p) {
 __device__ __forceinline__ f32x8 load8(const uint16_t* p) {
     return Mat<uint16_t>::unpack(__builtin_bit_cast(bf16x8, load16(p)));
 }
+// 8 channels as they are in memory.
+template <typename T> struct Raw8;
+template <> struct Raw8<uint16_t> {
+    u32x4 v;
+    __device__ __forceinline__ void load(const uint16_t* p) { v = load16(p); }
+    __device__ __forceinline__ void zero() { v = u32x4{0, 0, 0, 0}; }
+    __device__ __forceinline__ void set(int e, uint16_t x) { v[e / 2] |= uint32_t(x) << (16 * (e % 2)); }
+    __device__ __forceinline__ f32x8 f() const { return Mat<uint16_t>::unpack(__builtin_bit_cast(bf16x8, v)); }
+};
+template <> struct Raw8<float> {
+    f32x8 v;
+    __device__ __forceinline__ void load(const float* p) { v = load8(p); }
+    __device__ __forceinline__ void zero() { v = f32x8{0, 0, 0, 0, 0, 0, 0, 0}; }
+    __device__ __forceinline__ void set(int e, float x) { v[e] = x; }
+    __device__ __forceinline__ f32x8 f() const { return v; }
+};
 __device__ __forceinline__ void store8(float* p, f32x8 v) {
     store16(p, __builtin_bit_cast(u32x4, f32x4{v[0], v[1], v[2], v[3]}));
     store16(p + 4, __builtin_bit_cast(u32x4, f32x4{v[4], v[5], v[6], v[7]}));
@@ -49,22 +66,29 @@ __device__ __forceinline__ void store8(uint16_t* p, f32x8 v) {
     store16(p, __builtin_bit_cast(u32x4, Mat<uint16_t>::pack(v)));
 }
 
-// The channels of one of a row's THREADS threads: vectors of 8, the last one
-// of a row perhaps partly beyond its gd channels.
-template <int THREADS>
+// The channels of one of a row's threads: vectors of 8, the last one of a row
+// perhaps partly beyond its gd channels.
+template <bool WAVE>
 struct Lanes {
-    static __device__ __forceinline__ int at(int k) { return (int(threadIdx.x) % THREADS + THREADS * k) * 8; }
+    static __device__ __forceinline__ int at(int k) {
+        return WAVE ? (int(threadIdx.x) % 64 + 64 * k) * 8 : (int(threadIdx.x) + int(blockDim.x) * k) * 8;
+    }
     template <typename T>
-    static __device__ __forceinline__ f32x8 load(const T* p, int k, int gd) {
-        f32x8 v = {0, 0, 0, 0, 0, 0, 0, 0};
+    static __device__ __forceinline__ Raw8<T> raw(const T* p, int k, int gd) {
+        Raw8<T> v;
+        v.zero();
         if (at(k) + 8 <= gd) {
-            v = load8(p + at(k));
+            v.load(p + at(k));
         } else if (at(k) < gd) {
 #pragma unroll
             for (int e = 0; e < 7; e++)
-                if (at(k) + e < gd) v[e] = Elem<T>::load(p, at(k) + e);
+                if (at(k) + e < gd) v.set(e, p[at(k) + e]);
         }
         return v;
+    }
+    template <typename T>
+    static __device__ __forceinline__ f32x8 load(const T* p, int k, int gd) {
+        return raw(p, k, gd).f();
     }
     template <typename T>
     static __device__ __forceinline__ void store(T* p, int k, int gd, f32x8 v) {
@@ -78,26 +102,32 @@ struct Lanes {
     }
 };
 
-// Sums of a and b over the THREADS threads of a row, in every one of them.
-template <int THREADS>
+// Waves on a SIMD that kernels of one vector a thread are held to the registers of: 8 forward, so that three
+// workgroups of a 5120-channel row are resident on a compute unit and their memory latencies overlap; backward as many
+// as leave the next row's loads in registers (5 spill 70 bytes in the residual norm: 473 us against 337 at 32768 x 2560).
+constexpr int residual_bwd_waves() { return 4; }
+template <typename T>
+constexpr int gated_bwd_waves() { return sizeof(T) == 2 ? 5 : 4; }
+constexpr int kMaxRowWaves = 16;
+
+// Sums of a and b over a row's threads, in every one of them.
+template <bool WAVE>
 __device__ __forceinline__ void row_sums(float& a, float& b, float* red) {
     a = sum_wave(a);
     b = sum_wave(b);
-    if constexpr (THREADS > 64) {
-        constexpr int W = THREADS / 64;
-        const int wave = int(threadIdx.x) >> 6;
+    if constexpr (!WAVE) {
+        const int wave = int(threadIdx.x) >> 6, waves = int(blockDim.x) >> 6;
         __syncthreads();
         if ((threadIdx.x & 63) == 0) {
             red[wave] = a;
-            red[W + wave] = b;
+            red[kMaxRowWaves + wave] = b;
         }
         __syncthreads();
         a = red[0];
-        b = red[W];
-#pragma unroll
-        for (int i = 1; i < W; i++) {
+        b = red[kMaxRowWaves];
+        for (int i = 1; i < waves; i++) {
             a += red[i];
-            b += red[W + i];
+            b += red[kMaxRowWaves + i];
         }
     }
 }
@@ -117,13 +147,13 @@ __device__ __forceinline__ float scaled_sum(float res, float x, float scale) {
 template <typename T>
 __device__ __forceinline__ float stored(float v) { return widen(narrow<T>(v)); }
 
-template <typename T, typename TR, int THREADS, int VPT>
-__global__ __launch_bounds__(THREADS > 256 ? THREADS : 256) void residual_norm_fwd(NormParams p) {
-    using Ln = Lanes<THREADS>;
-    constexpr int RPW = THREADS == 64 ? 4 : 1;   // rows per workgroup
-    __shared__ float red[2 * (THREADS > 64 ? THREADS / 64 : 1)];
+template <typename T, typename TR, bool WAVE, int VPT>
+__global__ __launch_bounds__(WAVE ? 256 : 1024, VPT == 1 ? 8 : 1) void residual_norm_fwd(NormParams p) {
+    using Ln = Lanes<WAVE>;
+    constexpr int RPW = WAVE ? 4 : 1;   // rows per workgroup
+    __shared__ float red[WAVE ? 1 : 2 * kMaxRowWaves];
     const int gd = p.gd;
-    for (int64_t row = int64_t(blockIdx.x) * RPW + threadIdx.x / THREADS; row < p.rows; row += int64_t(gridDim.x) * RPW) {
+    for (int64_t row = int64_t(blockIdx.x) * RPW + (WAVE ? threadIdx.x / 64 : 0); row < p.rows; row += int64_t(gridDim.x) * RPW) {
         f32x8 r[VPT];
         float sq = 0.0f, unused = 0.0f;
 #pragma unroll
@@ -145,7 +175,7 @@ __global__ __launch_bounds__(THREADS > 256 ? THREADS : 256) void residual_norm_f
             r[k] = v;
             Ln::store(static_cast<TR*>(p.res_out) + row * p.d, k, gd, v);
         }
-        row_sums<THREADS>(sq, unused, red);
+        row_sums<WAVE>(sq, unused, red);
         const float inv = inv_rms(sq, gd, p.eps);
 #pragma unroll
         for (int k = 0; k < VPT; k++) {
@@ -155,24 +185,48 @@ __global__ __launch_bounds__(THREADS > 256 ? THREADS : 256) void residual_norm_f
     }
 }
 
-template <typename T, typename TR, int THREADS, int VPT>
-__global__ __launch_bounds__(THREADS > 256 ? THREADS : 256) void residual_norm_bwd(NormParams p) {
-    using Ln = Lanes<THREADS>;
-    constexpr int RPW = THREADS == 64 ? 4 : 1;
-    __shared__ float red[2 * (THREADS > 64 ? THREADS / 64 : 1)];
+template <typename T, typename TR, bool WAVE, int VPT>
+__global__ __launch_bounds__(WAVE ? 256 : 1024, VPT == 1 ? residual_bwd_waves() : 1) void residual_norm_bwd(NormParams p) {
+    using Ln = Lanes<WAVE>;
+    constexpr int RPW = WAVE ? 4 : 1;
+    __shared__ float red[WAVE ? 1 : 2 * kMaxRowWaves];
     const int gd = p.gd;
-    const int part = int(blockIdx.x) * RPW + int(threadIdx.x) / THREADS;
+    const int part = int(blockIdx.x) * RPW + (WAVE ? int(threadIdx.x) / 64 : 0);
     if (part >= p.parts) return;   // whole waves of a workgroup whose rows share nothing
     f32x8 dw[VPT], ds[VPT];
 #pragma unroll
     for (int k = 0; k < VPT; k++) dw[k] = ds[k] = f32x8{0, 0, 0, 0, 0, 0, 0, 0};
+    // The next row's loads are under way while a row is reduced.
+    Raw8<TR> next_r[VPT], next_dr[VPT];
+    Raw8<T> next_g[VPT], next_x[VPT];
+    auto fetch = [&](int64_t row) {
+#pragma unroll
+        for (int k = 0; k < VPT; k++) {
+            next_r[k] = Ln::raw(static_cast<const TR*>(p.res) + row * p.d, k, gd);
+            next_g[k] = Ln::raw(static_cast<const T*>(p.dout) + row * p.d, k, gd);
+            if (p.dres_out) next_dr[k] = Ln::raw(static_cast<const TR*>(p.dres_out) + row * p.d, k, gd);
+            if (p.scale) next_x[k] = Ln::raw(static_cast<const T*>(p.x) + row * p.xs, k, gd);
+        }
+    };
+#pragma unroll
+    for (int k = 0; k < VPT; k++) {
+        next_dr[k].zero();
+        next_x[k].zero();
+    }
+    fetch(part);
     for (int64_t row = part; row < p.rows; row += p.parts) {
-        f32x8 r[VPT], g[VPT];
+        f32x8 r[VPT], g[VPT], dr[VPT], x[VPT];
+#pragma unroll
+        for (int k = 0; k < VPT; k++) {
+            r[k] = next_r[k].f();
+            g[k] = next_g[k].f();
+            dr[k] = next_dr[k].f();
+            x[k] = next_x[k].f();
+        }
+        if (row + p.parts < p.rows) fetch(row + p.parts);
         float sq = 0.0f, ev = 0.0f;
 #pragma unroll
         for (int k = 0; k < VPT; k++) {
-            r[k] = Ln::load(static_cast<const TR*>(p.res) + row * p.d, k, gd);
-            g[k] = Ln::load(static_cast<const T*>(p.dout) + row * p.d, k, gd);
             const f32x8 w = Ln::load(p.w, k, gd);
 #pragma unroll
             for (int e = 0; e < 8; e++) {
@@ -180,21 +234,19 @@ __global__ __launch_bounds__(THREADS > 256 ? THREADS : 256) void residual_norm_b
                 ev += g[k][e] * w[e] * r[k][e];
             }
         }
-        row_sums<THREADS>(sq, ev, red);
+        row_sums<WAVE>(sq, ev, red);
         const float inv = inv_rms(sq, gd, p.eps), coef = inv * inv * (ev / float(gd));
 #pragma unroll
         for (int k = 0; k < VPT; k++) {
             const f32x8 w = Ln::load(p.w, k, gd);
-            f32x8 dr = {0, 0, 0, 0, 0, 0, 0, 0};
-            if (p.dres_out) dr = Ln::load(static_cast<const TR*>(p.dres_out) + row * p.d, k, gd);
-            dr += (g[k] * w - r[k] * coef) * inv;
+            dr[k] += (g[k] * w - r[k] * coef) * inv;
             dw[k] += g[k] * r[k] * inv;
-            if (p.dres) Ln::store(static_cast<TR*>(p.dres) + row * p.d, k, gd, dr);
+            if (p.dres) Ln::store(static_cast<TR*>(p.dres) + row * p.d, k, gd, dr[k]);
             if (p.scale) {
-                ds[k] += dr * Ln::load(static_cast<const T*>(p.x) + row * p.xs, k, gd);
-                dr *= Ln::load(p.scale, k, gd);
+                ds[k] += dr[k] * x[k];
+                dr[k] *= Ln::load(p.scale, k, gd);
             }
-            Ln::store(static_cast<T*>(p.dx) + row * p.d, k, gd, dr);
+            Ln::store(static_cast<T*>(p.dx) + row * p.d, k, gd, dr[k]);
         }
     }
     float* const to = p.part + int64_t(part) * p.d;
@@ -207,13 +259,13 @@ __global__ __launch_bounds__(THREADS > 256 ? THREADS : 256) void residual_norm_b
 
 __device__ __forceinline__ float sigmoid(float z) { return rcp_hw(1.0f + exp2_hw(-z * kLog2e)); }
 
-template <typename T, int THREADS, int VPT>
-__global__ __launch_bounds__(THREADS > 256 ? THREADS : 256) void gated_norm_fwd(NormParams p) {
-    using Ln = Lanes<THREADS>;
-    constexpr int RPW = THREADS == 64 ? 4 : 1;
-    __shared__ float red[2 * (THREADS > 64 ? THREADS / 64 : 1)];
+template <typename T, bool WAVE, int VPT>
+__global__ __launch_bounds__(WAVE ? 256 : 1024, VPT == 1 ? 8 : 1) void gated_norm_fwd(NormParams p) {
+    using Ln = Lanes<WAVE>;
+    constexpr int RPW = WAVE ? 4 : 1;
+    __shared__ float red[WAVE ? 1 : 2 * kMaxRowWaves];
     const int gd = p.gd;
-    for (int64_t at = int64_t(blockIdx.x) * RPW + threadIdx.x / THREADS; at < p.rows * p.groups;
+    for (int64_t at = int64_t(blockIdx.x) * RPW + (WAVE ? threadIdx.x / 64 : 0); at < p.rows * p.groups;
          at += int64_t(gridDim.x) * RPW) {
         const int64_t row = at / p.groups;
         const int c0 = int(at % p.groups) * gd;   // the group's first channel
@@ -230,7 +282,7 @@ __global__ __launch_bounds__(THREADS > 256 ? THREADS : 256) void gated_norm_fwd(
                 sq += v[k][e] * v[k][e];
             }
         }
-        row_sums<THREADS>(sq, unused, red);
+        row_sums<WAVE>(sq, unused, red);
         const float inv = inv_rms(sq, gd, p.eps);
 #pragma unroll
         for (int k = 0; k < VPT; k++) {
@@ -241,26 +293,40 @@ __global__ __launch_bounds__(THREADS > 256 ? THREADS : 256) void gated_norm_fwd(
     }
 }
 
-template <typename T, int THREADS, int VPT>
-__global__ __launch_bounds__(THREADS > 256 ? THREADS : 256) void gated_norm_bwd(NormParams p) {
-    using Ln = Lanes<THREADS>;
-    constexpr int RPW = THREADS == 64 ? 4 : 1;
-    __shared__ float red[2 * (THREADS > 64 ? THREADS / 64 : 1)];
+template <typename T, bool WAVE, int VPT>
+__global__ __launch_bounds__(WAVE ? 256 : 1024, VPT == 1 ? gated_bwd_waves<T>() : 1) void gated_norm_bwd(NormParams p) {
+    using Ln = Lanes<WAVE>;
+    constexpr int RPW = WAVE ? 4 : 1;
+    __shared__ float red[WAVE ? 1 : 2 * kMaxRowWaves];
     const int gd = p.gd;
-    const int64_t unit = int64_t(blockIdx.x) * RPW + threadIdx.x / THREADS;
+    const int64_t unit = int64_t(blockIdx.x) * RPW + (WAVE ? threadIdx.x / 64 : 0);
     if (unit >= int64_t(p.parts) * p.groups) return;
     const int part = int(unit / p.groups), c0 = int(unit % p.groups) * gd;
     f32x8 dw[VPT];
 #pragma unroll
     for (int k = 0; k < VPT; k++) dw[k] = f32x8{0, 0, 0, 0, 0, 0, 0, 0};
+    Raw8<T> next_y[VPT], next_z[VPT], next_g[VPT];   // the next row's, under way while a row is reduced
+    auto fetch = [&](int64_t row) {
+#pragma unroll
+        for (int k = 0; k < VPT; k++) {
+            next_y[k] = Ln::raw(static_cast<const T*>(p.x) + row * p.xs + c0, k, gd);
+            next_z[k] = Ln::raw(static_cast<const T*>(p.z) + row * p.zs + c0, k, gd);
+            next_g[k] = Ln::raw(static_cast<const T*>(p.dout) + row * p.d + c0, k, gd);
+        }
+    };
+    fetch(part);
     for (int64_t row = part; row < p.rows; row += p.parts) {
         f32x8 y[VPT], z[VPT], g[VPT];
+#pragma unroll
+        for (int k = 0; k < VPT; k++) {
+            y[k] = next_y[k].f();
+            z[k] = next_z[k].f();
+            g[k] = next_g[k].f();
+        }
+        if (row + p.parts < p.rows) fetch(row + p.parts);
         float sq = 0.0f, ev = 0.0f;
 #pragma unroll
         for (int k = 0; k < VPT; k++) {
-            y[k] = Ln::load(static_cast<const T*>(p.x) + row * p.xs + c0, k, gd);
-            z[k] = Ln::load(static_cast<const T*>(p.z) + row * p.zs + c0, k, gd);
-            g[k] = Ln::load(static_cast<const T*>(p.dout) + row * p.d + c0, k, gd);
             const f32x8 w = Ln::load(p.w + c0, k, gd);
 #pragma unroll
             for (int e = 0; e < 8; e++) {
@@ -271,7 +337,7 @@ __global__ __launch_bounds__(THREADS > 256 ? THREADS : 256) void gated_norm_bwd(
                 ev += en * v;
             }
         }
-        row_sums<THREADS>(sq, ev, red);
+        row_sums<WAVE>(sq, ev, red);
         const float inv = inv_rms(sq, gd, p.eps), coef = inv * inv * (ev / float(gd));
 #pragma unroll
         for (int k = 0; k < VPT; k++) {
@@ -307,8 +373,17 @@ __global__ __launch_bounds__(1024) void norm_sum_parts(const float* src, float* 
     const int s = int(threadIdx.x) >> 6;
     if (blockIdx.y == 1) src += int64_t(parts) * d;
     float v = 0.0f;
-    if (c < d)
-        for (int i = s; i < parts; i += 16) v += src[int64_t(i) * d + c];
+    if (c < d) {
+        int i = s;
+        for (; i + 7 * 16 < parts; i += 8 * 16) {   // eight loads at a time
+            float u[8];
+#pragma unroll
+            for (int k = 0; k < 8; k++) u[k] = src[int64_t(i + 16 * k) * d + c];
+#pragma unroll
+            for (int k = 0; k < 8; k++) v += u[k];
+        }
+        for (; i < parts; i += 16) v += src[int64_t(i) * d + c];
+    }
     share[s][threadIdx.x & 63] = v;
     __syncthreads();
     if (s == 0 && c < d) {

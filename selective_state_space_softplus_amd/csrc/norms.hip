@@ -11,33 +11,41 @@ using ss::NormParams;
 
 constexpr int64_t kMaxRows = (int64_t(1) << 31) - 1;
 
-// Threads and vectors per thread of a row of `gd` channels: a wave up to 1024
-// channels (no barriers), a workgroup beyond; the row stays in registers.
+// A row of `gd` channels is a wave's up to 1024 of them (one or two vectors a
+// lane, no barriers), else a workgroup's of as many waves as it has 512-channel
+// pieces, and past 16 waves of two vectors a lane.
 template <typename F>
 void by_width(int gd, F&& f) {
     using std::integral_constant;
-    auto go = [&](auto threads, auto vpt) { f(threads, vpt); };
-    if (gd <= 512) go(integral_constant<int, 64>{}, integral_constant<int, 1>{});
-    else if (gd <= 1024) go(integral_constant<int, 64>{}, integral_constant<int, 2>{});
-    else if (gd <= 2048) go(integral_constant<int, 256>{}, integral_constant<int, 1>{});
-    else if (gd <= 4096) go(integral_constant<int, 256>{}, integral_constant<int, 2>{});
-    else if (gd <= 8192) go(integral_constant<int, 256>{}, integral_constant<int, 4>{});
-    else go(integral_constant<int, 1024>{}, integral_constant<int, 2>{});
+    if (gd <= 512) f(std::true_type{}, integral_constant<int, 1>{});
+    else if (gd <= 1024) f(std::true_type{}, integral_constant<int, 2>{});
+    else if (gd <= 8192) f(std::false_type{}, integral_constant<int, 1>{});
+    else f(std::false_type{}, integral_constant<int, 2>{});
 }
 
 bool is_wave(int gd) { return gd <= 1024; }
-int block_threads(int gd) { return gd > 8192 ? 1024 : 256; }
+int block_threads(int gd) { return is_wave(gd) ? 256 : gd <= 8192 ? (gd + 511) / 512 * 64 : 1024; }
 
 unsigned fwd_grid(int64_t units, int gd) {
     const int64_t wgs = is_wave(gd) ? (units + 3) / 4 : units;
     return unsigned(std::min<int64_t>(wgs, int64_t(1) << 21));
 }
 
-// Shares of the sums over rows: enough walkers over the rows to fill the chip
-// (4 workgroups to a compute unit), each at least one row.
-int64_t row_parts(int64_t rows, int64_t gd, int64_t groups) {
-    const int64_t walkers = is_wave(int(gd)) ? 4096 : 1024;
-    return std::max<int64_t>(1, std::min<int64_t>(rows, walkers / groups));
+// Shares of the sums over rows: as many walkers over the rows as are resident
+// at once (`waves` on each SIMD of 256 compute units), each with at least 2 rows so that
+// the shares stay fewer than the rows.
+int64_t row_parts(int64_t rows, int64_t gd, int64_t groups, int waves) {
+    const int64_t a_unit = 4 * waves;   // waves on a compute unit
+    const int64_t walkers =
+        256 * (is_wave(int(gd)) ? a_unit : std::max<int64_t>(1, a_unit / (block_threads(int(gd)) / 64)));
+    return std::max<int64_t>(1, std::min<int64_t>((rows + 1) / 2, walkers / groups));
+}
+
+int64_t residual_parts(int64_t rows, int64_t d) { return row_parts(rows, d, 1, ss::residual_bwd_waves()); }
+
+int64_t gated_parts(int64_t rows, int64_t d, int64_t groups, int dtype) {
+    return row_parts(rows, d / groups, groups,
+                     dtype == SS_BF16 ? ss::gated_bwd_waves<uint16_t>() : ss::gated_bwd_waves<float>());
 }
 
 unsigned bwd_grid(int64_t units, int gd) { return unsigned(is_wave(gd) ? (units + 3) / 4 : units); }
@@ -55,15 +63,16 @@ int64_t extent(int64_t rows, int64_t d, int64_t stride) { return (rows - 1) * st
 
 template <typename T, typename TR>
 int run_residual(const NormParams& p, bool back, float* dweight, float* dscale, hipStream_t st) {
-    by_width(p.gd, [&](auto threads, auto vpt) {
-        constexpr int TH = decltype(threads)::value, V = decltype(vpt)::value;
+    by_width(p.gd, [&](auto wave, auto vpt) {
+        constexpr bool W = decltype(wave)::value;
+        constexpr int V = decltype(vpt)::value;
         const int block = block_threads(p.gd);
         if (!back) {
             const unsigned grid = fwd_grid(p.rows, p.gd);
-            ss::residual_norm_fwd<T, TR, TH, V><<<grid, block, 0, st>>>(p);
+            ss::residual_norm_fwd<T, TR, W, V><<<grid, block, 0, st>>>(p);
         } else {
             const unsigned grid = bwd_grid(p.parts, p.gd);
-            ss::residual_norm_bwd<T, TR, TH, V><<<grid, block, 0, st>>>(p);
+            ss::residual_norm_bwd<T, TR, W, V><<<grid, block, 0, st>>>(p);
         }
     });
     if (back)
@@ -81,15 +90,16 @@ int dispatch_residual(const NormParams& p, int dtype, int res_dtype, bool back, 
 
 template <typename T>
 int run_gated(const NormParams& p, bool back, float* dweight, hipStream_t st) {
-    by_width(p.gd, [&](auto threads, auto vpt) {
-        constexpr int TH = decltype(threads)::value, V = decltype(vpt)::value;
+    by_width(p.gd, [&](auto wave, auto vpt) {
+        constexpr bool W = decltype(wave)::value;
+        constexpr int V = decltype(vpt)::value;
         const int block = block_threads(p.gd);
         if (!back) {
             const unsigned grid = fwd_grid(p.rows * p.groups, p.gd);
-            ss::gated_norm_fwd<T, TH, V><<<grid, block, 0, st>>>(p);
+            ss::gated_norm_fwd<T, W, V><<<grid, block, 0, st>>>(p);
         } else {
             const unsigned grid = bwd_grid(int64_t(p.parts) * p.groups, p.gd);
-            ss::gated_norm_bwd<T, TH, V><<<grid, block, 0, st>>>(p);
+            ss::gated_norm_bwd<T, W, V><<<grid, block, 0, st>>>(p);
         }
     });
     if (back)
@@ -133,7 +143,7 @@ SS_EXPORT int ss_residual_norm_fwd(const void* x, const void* residual, const fl
 
 SS_EXPORT size_t ss_residual_norm_bwd_workspace_bytes(int64_t rows, int64_t d) {
     if (check_norm(rows, d, 1, 0.0) != SS_OK) return 0;
-    return round256(2 * size_t(row_parts(rows, d, 1)) * size_t(d) * sizeof(float));
+    return round256(2 * size_t(residual_parts(rows, d)) * size_t(d) * sizeof(float));
 }
 
 SS_EXPORT int ss_residual_norm_bwd(const void* dout, const void* dresidual_out, const void* residual_out,
@@ -180,7 +190,7 @@ SS_EXPORT int ss_residual_norm_bwd(const void* dout, const void* dresidual_out, 
     p.xs = x_stride;
     p.gd = int(d);
     p.groups = 1;
-    p.parts = int(row_parts(rows, d, 1));
+    p.parts = int(residual_parts(rows, d));
     p.eps = float(eps);
     return dispatch_residual(p, dtype, res_dtype, true, dweight, dscale, static_cast<hipStream_t>(stream));
 }
@@ -218,7 +228,8 @@ SS_EXPORT int ss_gated_norm_fwd(const void* y, const void* z, const float* weigh
 
 SS_EXPORT size_t ss_gated_norm_bwd_workspace_bytes(int64_t rows, int64_t d, int64_t groups) {
     if (check_norm(rows, d, groups, 0.0) != SS_OK) return 0;
-    return round256(size_t(row_parts(rows, d / groups, groups)) * size_t(d) * sizeof(float));
+    return round256(size_t(std::max(gated_parts(rows, d, groups, SS_BF16), gated_parts(rows, d, groups, SS_F32))) *
+                    size_t(d) * sizeof(float));
 }
 
 SS_EXPORT int ss_gated_norm_bwd(const void* dout, const void* y, const void* z, const float* weight, void* dy,
@@ -256,7 +267,7 @@ SS_EXPORT int ss_gated_norm_bwd(const void* dout, const void* y, const void* z, 
     p.zs = z_stride;
     p.groups = int(groups);
     p.gd = int(d / groups);
-    p.parts = int(row_parts(rows, d / groups, groups));
+    p.parts = int(gated_parts(rows, d, groups, dtype));
     p.eps = float(eps);
     p.before = norm_before_gate ? 1 : 0;
     const hipStream_t st = static_cast<hipStream_t>(stream);
