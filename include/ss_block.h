@@ -17,10 +17,11 @@
  *     S      = a * S + delta' * x[b,t,h,:] B[b,t,g,:]^T          (P x N, fp32)
  *     y      = S C[b,t,g,:] + D[h] * x[b,t,h,:]
  * A step's decay below 2^-200 is taken as 2^-200 (both are 0 in fp32).  Steps
- * are taken 64 at a time by matrix products.  With bf16 inputs the products
- * that carry the state, and the sums behind last_state and the gradients of
- * the fp32 parameters, are exact to fp32; the others round one operand to bf16
- * and sum in fp32.
+ * are taken 64 at a time by matrix products; where delta' < 0 (possible without
+ * softplus) makes the state grow, the growth over 64 steps has to stay in fp32's
+ * range.  With bf16 inputs the products behind last_state and
+ * dinitial_state are exact to fp32, those behind the other fp32 gradients to
+ * 2^-18 of an operand; the others round one operand to bf16.  All sum in fp32.
  */
 #ifndef SS_BLOCK_H
 #define SS_BLOCK_H

@@ -112,6 +112,9 @@ def _workspace(device, nbytes: int):
 
 def _check_tokens(t, name, shape, dtype, device):
     """As _check, for a tensor (b, L, ...) whose batch and time strides are free."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == device \
+            and t.is_contiguous():
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.device != device:
@@ -125,6 +128,9 @@ def _check_tokens(t, name, shape, dtype, device):
         if size != 1 and stride != inner:
             raise ValueError(f"{name} must have each token's elements contiguous")
         inner *= size
+
+
+_Strides = ctypes.c_int64 * 8
 
 
 def _head_args(x, delta, A_log, B, C, D, delta_bias, initial_state):
@@ -143,7 +149,9 @@ def _head_args(x, delta, A_log, B, C, D, delta_bias, initial_state):
     _check(D, "D", (H,), torch.float32, dev)
     _check(delta_bias, "delta_bias", (H,), torch.float32, dev)
     _check(initial_state, "initial_state", (b, H, P, N), torch.float32, dev)
-    strides = (ctypes.c_int64 * 8)(*(s for t in (x, delta, B, C) for s in t.stride()[:2]))
+    strides = None
+    if not (x.is_contiguous() and delta.is_contiguous() and B.is_contiguous() and C.is_contiguous()):
+        strides = _Strides(*x.stride()[:2], *delta.stride()[:2], *B.stride()[:2], *C.stride()[:2])
     return b, L, H, P, N, G, dev, _dtype_code(x.dtype), strides
 
 
@@ -158,7 +166,8 @@ def head_scan_fwd(x, delta, A_log, B, C, D, delta_bias=None, delta_softplus=True
     ``initial_state`` may be the ``last_state`` buffer itself (carried over in place).
     """
     b, L, H, P, N, G, dev, code, strides = _head_args(x, delta, A_log, B, C, D, delta_bias, initial_state)
-    y = torch.empty((b, L, H, P), dtype=x.dtype, device=dev) if out is None else out
+    y = (torch.empty_like(x) if strides is None else torch.empty((b, L, H, P), dtype=x.dtype, device=dev)) \
+        if out is None else out
     _check(y, "out", (b, L, H, P), x.dtype, dev)
     if return_last_state and last_state is None:
         last_state = torch.empty((b, H, P, N), dtype=torch.float32, device=dev)
@@ -273,7 +282,10 @@ def head_state_update(state, x, dt, A_log, B, C, D, dt_bias=None, dt_softplus=Tr
 
 
 def _rows(t, name, shape, dtype, device):
-    """Rows and row stride of a tensor whose rows (last dimension) are contiguous and evenly spaced."""
+    """Row stride of a tensor whose rows (last dimension) are contiguous and evenly spaced."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == device \
+            and t.is_contiguous():
+        return t.shape[-1]
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.device != device:
@@ -325,8 +337,9 @@ def residual_norm_fwd(x, weight, residual=None, scale=None, eps=1e-5, residual_d
     _check(weight, "weight", (d,), torch.float32, dev)
     _check(residual, "residual", x.shape, rt, dev)
     _check(scale, "scale", (d,), torch.float32, dev)
-    out = torch.empty(x.shape, dtype=x.dtype, device=dev) if out is None else out
-    residual_out = torch.empty(x.shape, dtype=rt, device=dev) if residual_out is None else residual_out
+    out = torch.empty_like(x, memory_format=torch.contiguous_format) if out is None else out
+    if residual_out is None:
+        residual_out = torch.empty_like(x, memory_format=torch.contiguous_format, dtype=rt)
     _check(out, "out", x.shape, x.dtype, dev)
     _check(residual_out, "residual_out", x.shape, rt, dev)
     if rows == 0 or d == 0:
@@ -409,7 +422,7 @@ def gated_norm_fwd(y, z, weight, groups=1, eps=1e-5, norm_before_gate=False, out
     y_stride = _rows(y, "y", y.shape, y.dtype, dev)
     z_stride = _rows(z, "z", y.shape, y.dtype, dev)
     _check(weight, "weight", (d,), torch.float32, dev)
-    out = torch.empty(y.shape, dtype=y.dtype, device=dev) if out is None else out
+    out = torch.empty_like(y, memory_format=torch.contiguous_format) if out is None else out
     _check(out, "out", y.shape, y.dtype, dev)
     if rows == 0 or d == 0:
         return out

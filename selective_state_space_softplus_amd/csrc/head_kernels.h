@@ -435,12 +435,20 @@ __global__ __launch_bounds__(256) void head_carry(HeadParams p) {
     const float* const init = REV ? p.dlast : p.h0;
     float s = init && inside ? init[(bh * p.P + pg) * p.N + n] : 0.0f;
     float* const states = p.seg_state + bhs * p.nseg * (NP * 64) + (at & (NP * 64 - 1));
-    for (int i = 0; i < p.nseg; i++) {
-        const int seg = REV ? p.nseg - 1 - i : i;
-        float* const q = states + int64_t(seg) * (NP * 64);
-        const float next = i + 1 < p.nseg ? exp2_hw(p.seg_decay[bh * p.nseg + seg]) * s + *q : 0.0f;
-        *q = s;
-        s = next;
+    for (int i0 = 0; i0 < p.nseg; i0 += 8) {   // eight segments' loads at a time
+        float local[8], decay[8];
+#pragma unroll
+        for (int k = 0; k < 8; k++) {
+            const int i = min(i0 + k, p.nseg - 2), seg = REV ? p.nseg - 1 - i : i;   // the last one has neither
+            local[k] = states[int64_t(seg) * (NP * 64)];
+            decay[k] = p.seg_decay[bh * p.nseg + seg];
+        }
+#pragma unroll
+        for (int k = 0; k < 8; k++) {
+            const int i = i0 + k, seg = REV ? p.nseg - 1 - i : i;
+            if (i < p.nseg) states[int64_t(seg) * (NP * 64)] = s;
+            s = exp2_hw(decay[k]) * s + local[k];
+        }
     }
 }
 
