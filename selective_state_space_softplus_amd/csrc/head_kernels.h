@@ -111,6 +111,7 @@ struct GateLds {
 // 8 floats at p (16-byte aligned).
 __device__ __forceinline__ f32x8 floats8(const float* p) { return Mat<float>::load(p); }
 __device__ __forceinline__ f32x4 floats4(const float* p) { return *reinterpret_cast<const f32x4*>(p); }
+__device__ __forceinline__ f32x8 floats4_2(const float* p, const float* q) { return Mat<float>::load_2x4(p, q); }
 
 // Each wave's word of `flags` says whether one of its lanes met a non-finite value.
 __device__ __forceinline__ void note_non_finite(uint32_t* flags, bool met) {
@@ -207,65 +208,81 @@ struct Walk {
     __device__ __forceinline__ int64_t state_at(const HeadParams& p, int np, int64_t count, int64_t i) const {
         return (((bi * p.H + my_h) * p.slabs + my_slab) * count + i) * (np * 64);
     }
-    // Element (n, p0 + 16 ct + lane % 16) of this wave's job in a (b, H, P, N) tensor; -1 outside.
-    __device__ __forceinline__ int64_t out_at(const HeadParams& p, int n, int ct) const {
-        const int pg = my_slab * kHeadSlab + p0 + 16 * ct + int(threadIdx.x & 15);
+    // State n of this wave's channel pc in a (b, H, P, N) tensor; -1 outside.
+    __device__ __forceinline__ int64_t out_at(const HeadParams& p, int n, int pc) const {
+        const int pg = my_slab * kHeadSlab + p0 + pc;
         return n < p.N && pg < p.P ? ((bi * p.H + my_h) * p.P + pg) * p.N + n : -1;
     }
 };
 
-// The wave's state from / to a padded (NP, 64) tile.
-template <int NP, int JOBS>
-__device__ __forceinline__ void state_load(f32x4 (&acc)[JOBS][NP / 16], const float* src, int p0) {
-    const int lane = threadIdx.x & 63;
+// How a wave's state lies in its accumulators.  Rows: lane group g holds states
+// n = 16 nt + 4 g + r of channel lane % 16, which is also how the readout takes
+// it as an operand.  Columns: state n = 16 nt + lane % 16 of channels 4 g + r,
+// four neighbours in memory, for the passes that only store states.
+enum class Lie { Rows, Columns };
+
+template <int NP, int JOBS, Lie LIE, typename F>
+__device__ __forceinline__ void each_state(int lane, F&& f) {
 #pragma unroll
     for (int ct = 0; ct < JOBS; ct++)
 #pragma unroll
         for (int nt = 0; nt < NP / 16; nt++)
 #pragma unroll
-            for (int r = 0; r < 4; r++)
-                acc[ct][nt][r] = src[(16 * nt + lane / 16 * 4 + r) * 64 + p0 + 16 * ct + lane % 16];
+            for (int r = 0; r < 4; r++) {
+                const int n = 16 * nt + (LIE == Lie::Rows ? lane / 16 * 4 + r : lane % 16);
+                const int pc = 16 * ct + (LIE == Lie::Rows ? lane % 16 : lane / 16 * 4 + r);
+                f(ct, nt, r, n, pc);
+            }
+}
+
+// The wave's state from / to a padded (NP, 64) tile.
+template <int NP, int JOBS, Lie LIE>
+__device__ __forceinline__ void state_load(f32x4 (&acc)[JOBS][NP / 16], const float* src, int p0) {
+    each_state<NP, JOBS, LIE>(threadIdx.x & 63, [&](int ct, int nt, int r, int n, int pc) {
+        acc[ct][nt][r] = src[n * 64 + p0 + pc];
+    });
 }
 template <int NP, int JOBS>
 __device__ __forceinline__ void state_store(const f32x4 (&acc)[JOBS][NP / 16], float* dst, int p0) {
     const int lane = fresh_lane();
-    dst += lane / 16 * 256 + p0 + lane % 16;
+    dst += lane % 16 * 64 + p0 + lane / 16 * 4;
 #pragma unroll
-    for (int ct = 0; ct < JOBS; ct++)
+    for (int nt = 0; nt < NP / 16; nt++)
 #pragma unroll
-        for (int nt = 0; nt < NP / 16; nt++)
+        for (int ct = 0; ct < JOBS; ct++) *reinterpret_cast<f32x4*>(dst + nt * 1024 + 16 * ct) = acc[ct][nt];
+}
+// A chunk's state in memory: 16 x 16 tiles as their accumulators' lanes hold
+// them (Columns), so that one store is 1 KB in a row, and a lane of the
+// gradients still finds 4 neighbouring channels of its n together.  (Storing
+// [n][channel] instead fills the wave's 63 outstanding accesses and stops it:
+// 203 us against what it takes now, b = 1, L = 16384, H = 80.)
+__device__ __forceinline__ int tile_at(int n, int pc) {
+    return ((n >> 4) * 4 + (pc >> 4)) * 256 + ((pc >> 2 & 3) * 16 + (n & 15)) * 4 + (pc & 3);
+}
+template <int NP, int JOBS>
+__device__ __forceinline__ void state_store_tiles(const f32x4 (&acc)[JOBS][NP / 16], float* dst, int p0) {
+    dst += p0 / 16 * 256 + fresh_lane() * 4;
 #pragma unroll
-            for (int r = 0; r < 4; r++)
-                dst[(16 * nt + r) * 64 + 16 * ct] = acc[ct][nt][r];
+    for (int nt = 0; nt < NP / 16; nt++)
+#pragma unroll
+        for (int ct = 0; ct < JOBS; ct++) *reinterpret_cast<f32x4*>(dst + (nt * 4 + ct) * 256) = acc[ct][nt];
 }
 // The same from / to a (b, H, P, N) tensor; NULL reads as zero.
-template <int NP, int JOBS>
+template <int NP, int JOBS, Lie LIE>
 __device__ __forceinline__ void state_read(f32x4 (&acc)[JOBS][NP / 16], const HeadParams& p, const Walk<JOBS>& w,
                                            const float* src) {
-    const int lane = threadIdx.x & 63;
-#pragma unroll
-    for (int ct = 0; ct < JOBS; ct++)
-#pragma unroll
-        for (int nt = 0; nt < NP / 16; nt++)
-#pragma unroll
-            for (int r = 0; r < 4; r++) {
-                const int64_t at = w.out_at(p, 16 * nt + lane / 16 * 4 + r, ct);
-                acc[ct][nt][r] = src && at >= 0 ? src[at] : 0.0f;
-            }
+    each_state<NP, JOBS, LIE>(threadIdx.x & 63, [&](int ct, int nt, int r, int n, int pc) {
+        const int64_t at = w.out_at(p, n, pc);
+        acc[ct][nt][r] = src && at >= 0 ? src[at] : 0.0f;
+    });
 }
-template <int NP, int JOBS>
+template <int NP, int JOBS, Lie LIE>
 __device__ __forceinline__ void state_write(const f32x4 (&acc)[JOBS][NP / 16], const HeadParams& p,
                                             const Walk<JOBS>& w, float* dst) {
-    const int lane = threadIdx.x & 63;
-#pragma unroll
-    for (int ct = 0; ct < JOBS; ct++)
-#pragma unroll
-        for (int nt = 0; nt < NP / 16; nt++)
-#pragma unroll
-            for (int r = 0; r < 4; r++) {
-                const int64_t at = w.out_at(p, 16 * nt + lane / 16 * 4 + r, ct);
-                if (at >= 0) dst[at] = acc[ct][nt][r];
-            }
+    each_state<NP, JOBS, LIE>(threadIdx.x & 63, [&](int ct, int nt, int r, int n, int pc) {
+        const int64_t at = w.out_at(p, n, pc);
+        if (at >= 0) dst[at] = acc[ct][nt][r];
+    });
 }
 
 // acc = decay * acc + K^T (w V): K a tile [step][n], V the wave's columns of a
@@ -273,7 +290,7 @@ __device__ __forceinline__ void state_write(const f32x4 (&acc)[JOBS][NP / 16], c
 // PARTS bf16 operands: three where the state is an output, which makes it what
 // fp32 products would give (error against 64 bits 1e-7 relative); two where it
 // only feeds others (2e-6).
-template <typename T, int NP, int JOBS, int PARTS>
+template <typename T, int NP, int JOBS, int PARTS, Lie LIE>
 __device__ __forceinline__ void state_update(f32x4 (&acc)[JOBS][NP / 16], float decay, const T* k_lds,
                                              const typename Mat<T>::Frag (&vf)[JOBS][2], const float* weights,
                                              int lane) {
@@ -310,7 +327,9 @@ __device__ __forceinline__ void state_update(f32x4 (&acc)[JOBS][NP / 16], float 
 #pragma unroll
                 for (int ct = 0; ct < JOBS; ct++) M::template split<PARTS>(M::unpack(vf[ct][kk]) * wv[kk], w[ct]);
 #pragma unroll
-            for (int ct = 0; ct < JOBS; ct++) acc[ct][nt] = mma_wide<T, PARTS>(kf[i & 1][k], w[ct], acc[ct][nt]);
+            for (int ct = 0; ct < JOBS; ct++)
+                acc[ct][nt] = LIE == Lie::Rows ? mma_wide<T, PARTS>(kf[i & 1][k], w[ct], acc[ct][nt])
+                                               : wide_mma<T, PARTS>(w[ct], kf[i & 1][k], acc[ct][nt]);
         }
     }
 }
@@ -348,8 +367,8 @@ __global__ __launch_bounds__(256, 2) void head_states(HeadParams p) {
 
     f32x4 acc[JOBS][NP / 16];
     float* const seg_at = p.seg_state + w.state_at(p, NP, p.nseg, w.seg);
-    if (MODE == StateMode::Chunks && p.nseg > 1) state_load<NP, JOBS>(acc, seg_at, w.p0);
-    else state_read<NP, JOBS>(acc, p, w, MODE == StateMode::Chunks ? (REV ? p.dlast : p.h0) : nullptr);
+    if (MODE == StateMode::Chunks && p.nseg > 1) state_load<NP, JOBS, Lie::Columns>(acc, seg_at, w.p0);
+    else state_read<NP, JOBS, Lie::Columns>(acc, p, w, MODE == StateMode::Chunks ? (REV ? p.dlast : p.h0) : nullptr);
 
     TileK tk;
     TileV tv[JOBS];
@@ -398,7 +417,7 @@ __global__ __launch_bounds__(256, 2) void head_states(HeadParams p) {
         const bool entry = steps.lo == 0, done = steps.next(rows);
         if (done && it + 1 < count) fetch(REV ? ck - 1 : ck + 1);
         if (MODE == StateMode::Chunks && entry && w.my_alive)
-            state_store<NP, JOBS>(acc, (REV ? p.chunk_q : p.chunk_s) + w.state_at(p, NP, p.chunks, ck), w.p0);
+            state_store_tiles<NP, JOBS>(acc, (REV ? p.chunk_q : p.chunk_s) + w.state_at(p, NP, p.chunks, ck), w.p0);
         typename M::Frag vf[JOBS][2];
 #pragma unroll
         for (int ct = 0; ct < JOBS; ct++)
@@ -408,7 +427,7 @@ __global__ __launch_bounds__(256, 2) void head_states(HeadParams p) {
         const GateLds& gt = gates[w.job];
         const float cq = gt.c[63].x;
         total += cq;
-        state_update<T, NP, JOBS, PARTS>(acc, exp2_hw(cq), k_lds, vf, REV ? gt.in : gt.out, lane);
+        state_update<T, NP, JOBS, PARTS, Lie::Columns>(acc, exp2_hw(cq), k_lds, vf, REV ? gt.in : gt.out, lane);
         if (done) it++;
     }
     if (!w.my_alive) return;
@@ -416,7 +435,7 @@ __global__ __launch_bounds__(256, 2) void head_states(HeadParams p) {
         state_store<NP, JOBS>(acc, seg_at, w.p0);
         if (w.my_slab == 0 && lane == 0) p.seg_decay[(w.bi * p.H + w.my_h) * p.nseg + w.seg] = total;
     } else if (REV && w.seg == 0 && p.dh0) {
-        state_write<NP, JOBS>(acc, p, w, p.dh0);
+        state_write<NP, JOBS, Lie::Columns>(acc, p, w, p.dh0);
     }
 }
 
@@ -484,8 +503,8 @@ __global__ __launch_bounds__(256, 2) void head_out(HeadParams p) {
     const float skip = p.D[w.my_h];
 
     f32x4 acc[JOBS][NP / 16];
-    if (p.nseg > 1) state_load<NP, JOBS>(acc, p.seg_state + w.state_at(p, NP, p.nseg, w.seg), w.p0);
-    else state_read<NP, JOBS>(acc, p, w, p.h0);
+    if (p.nseg > 1) state_load<NP, JOBS, Lie::Rows>(acc, p.seg_state + w.state_at(p, NP, p.nseg, w.seg), w.p0);
+    else state_read<NP, JOBS, Lie::Rows>(acc, p, w, p.h0);
 
     TileK tb, tc;
     TileV tx[JOBS];
@@ -672,12 +691,12 @@ __global__ __launch_bounds__(256, 2) void head_out(HeadParams p) {
 #pragma unroll
             for (int it = 0; it < 4; it++) store4(at + 16 * it * TileV::kLd, out[ct][it] + skip * xd[it]);
         }
-        state_update<T, NP, JOBS, PARTS>(acc, exp2_hw(gt.c[63].x), b_lds, xf, gt.out, lane);
+        state_update<T, NP, JOBS, PARTS, Lie::Rows>(acc, exp2_hw(gt.c[63].x), b_lds, xf, gt.out, lane);
         if (done) ck++;
     }
     barrier_lds();
     write_y(out_ck, out_lo, out_hi);
-    if (w.seg == p.nseg - 1 && p.last && w.my_alive) state_write<NP, JOBS>(acc, p, w, p.last);
+    if (w.seg == p.nseg - 1 && p.last && w.my_alive) state_write<NP, JOBS, Lie::Rows>(acc, p, w, p.last);
 }
 
 // Gradients of one chunk for the heads of one head block of a group.
@@ -787,11 +806,12 @@ __global__ __launch_bounds__(512, 2) void head_grad(HeadParams p) {
         return (((bi * p.H + h) * p.slabs + slab) * p.chunks + ck) * (NP * 64);
     };
     auto fetch_states = [&](int h, int slab) {
-        const int64_t at = state_at(h, slab) + n * 64 + 8 * lg;
+        const int lane = fresh_lane(), lg = lane >> 4;
+        const int64_t at = state_at(h, slab) + tile_at(16 * nt + (lane & 15), 8 * lg);
 #pragma unroll
         for (int kk = 0; kk < 2; kk++) {
-            sv[kk] = floats8(p.chunk_s + at + 32 * kk);
-            qv[kk] = floats8(p.chunk_q + at + 32 * kk);
+            sv[kk] = floats4_2(p.chunk_s + at + 512 * kk, p.chunk_s + at + 512 * kk + 64);
+            qv[kk] = floats4_2(p.chunk_q + at + 512 * kk, p.chunk_q + at + 512 * kk + 64);
         }
     };
     fetch(h_first, 0);
@@ -1023,9 +1043,9 @@ __global__ __launch_bounds__(512, 2) void head_grad(HeadParams p) {
                 if constexpr (sizeof(T) == 2) {
                     qb[kk] = M::columns(lds.q, kLdV, 32 * kk, dp, lane);
                 } else {
-                    const float* const q = p.chunk_q + state_at(h, slab) + (32 * kk + 8 * lg) * 64 + dp + lr;
+                    const float* const q = p.chunk_q + state_at(h, slab) + tile_at(32 * kk + 8 * lg, dp + lr);
 #pragma unroll
-                    for (int e = 0; e < 8; e++) qb[kk][e] = q[e * 64];
+                    for (int e = 0; e < 8; e++) qb[kk][e] = q[e * 4];
                 }
             }
 #pragma unroll
