@@ -518,7 +518,6 @@ __global__ __launch_bounds__(256, 2) void head_out(HeadParams p) {
         for (int k = 0; k < JOBS; k++)
             tx[k].load(xb + t0 * p.xt + int64_t(w.h[k]) * p.P + w.slab[k] * kHeadSlab, p.xt, rows,
                        p.P - w.slab[k] * kHeadSlab, w.slab[k] * kHeadSlab);
-        dl = gate_load<T>(p, w.bi, gate_head, ck);
     };
     auto fetch_short = [&](int ck, int rows) {
         const int64_t t0 = int64_t(ck) * kHeadChunk;
@@ -542,9 +541,17 @@ __global__ __launch_bounds__(256, 2) void head_out(HeadParams p) {
     };
     T* const xj = x_lds + w.job * TileV::kElems;
     const T* const mj = m_lds + w.job * TileV::kElems;
-    const GateLds& gt = gates[w.job];
+    // The gates of a chunk are formed a chunk ahead, by the waves that have the fewest score tiles.
+    auto gates_at = [&](int ck) { return gates + (ck & 1) * JOBS; };
+    auto put_gates = [&](int ck, const Steps& steps, int lane) {
+        if (wave < JOBS)
+            gates_at(ck)[wave].put(make_gate(Raw<T>::f(dl), bias, a2, p.softplus, steps.has(lane, chunk_rows(p, ck))));
+    };
     fetch(w.first);
+    dl = gate_load<T>(p, w.bi, gate_head, w.first);
     Steps steps;
+    put_gates(w.first, steps, threadIdx.x & 63);
+    dl = gate_load<T>(p, w.bi, gate_head, min(w.first + 1, w.last));
     int out_ck = -1, out_lo = 0, out_hi = 0;   // the outputs in x_lds
     for (int ck = w.first; ck <= w.last;) {
         const int lane = fresh_lane(), lr = lane & 15, lg = lane >> 4;
@@ -562,17 +569,28 @@ __global__ __launch_bounds__(256, 2) void head_out(HeadParams p) {
                         w.slab[k] * kHeadSlab);
             met |= tx[k].non_finite();
         }
-        if (wave < JOBS) gates[wave].put(make_gate(Raw<T>::f(dl), bias, a2, p.softplus, steps.has(lane, rows)));
+        if (steps.single) {   // its own gates, step by step
+            dl = gate_load<T>(p, w.bi, gate_head, ck);
+            put_gates(ck, steps, lane);
+        }
         note_non_finite(gates[0].flags, met);
         barrier_lds();
         if (!steps.single && any_noted(gates[0].flags)) {
             steps.begin();
             continue;
         }
+        const bool was_single = steps.single;
+        GateLds* const now = gates_at(ck);
+        const GateLds& gt = now[w.job];
         out_ck = ck;
         out_lo = steps.lo;
         out_hi = steps.end(rows);
         const bool done = steps.next(rows);
+        if (done && ck < w.last) {
+            if (was_single) dl = gate_load<T>(p, w.bi, gate_head, ck + 1);
+            put_gates(ck + 1, steps, lane);
+            dl = gate_load<T>(p, w.bi, gate_head, min(ck + 2, w.last));
+        }
 
         // Scores of rows i = 16 wave + lr, columns j = 16 jt + 4 lg + r; those of j > i are zeros.
         const int i_row = 16 * wave + lr;
@@ -615,15 +633,15 @@ __global__ __launch_bounds__(256, 2) void head_out(HeadParams p) {
         // Weighted: exp(c_i - c_j) s_j as exp(c_i - c_e) tail_j with e the last step of tile jt < it, neither above 1.
 #pragma unroll
         for (int k = 0; k < JOBS; k++) {
-            const f32x2 ci = gates[k].c[i_row];
-            const float* const cj = reinterpret_cast<const float*>(gates[k].c + 16 * wave + 4 * lg);
-            const f32x4 c01 = floats4(cj), c23 = floats4(cj + 4), sj = floats4(gates[k].step + 16 * wave + 4 * lg);
+            const f32x2 ci = now[k].c[i_row];
+            const float* const cj = reinterpret_cast<const float*>(now[k].c + 16 * wave + 4 * lg);
+            const f32x4 c01 = floats4(cj), c23 = floats4(cj + 4), sj = floats4(now[k].step + 16 * wave + 4 * lg);
             f32x2 ce[3];
             f32x4 tail[3];
 #pragma unroll
             for (int jt = 0; jt < 3; jt++) {
-                ce[jt] = gates[k].c[16 * jt + 15];
-                tail[jt] = floats4(gates[k].tail + 16 * jt + 4 * lg);
+                ce[jt] = now[k].c[16 * jt + 15];
+                tail[jt] = floats4(now[k].tail + 16 * jt + 4 * lg);
             }
             issue_loads<T>();
             T* const mi = m_lds + k * TileV::kElems + i_row * TileV::kLd + 4 * lg;
@@ -721,8 +739,8 @@ __global__ __launch_bounds__(256, 2) void head_out(HeadParams p) {
 // The scores' 64 x 64 tile goes to the waves by two 16 x 16 pieces, dB and dC
 // (accumulated over heads in registers) by 16 columns n, dx by 16 columns and
 // 32 rows.  Two barriers a head: x, dy and the gates have two places in LDS,
-// and so have the shares of the sums, which wave 0 turns into ddelta while the
-// others are at the next head's scores.
+// and so have the shares of the sums, which a wave without scores turns into
+// ddelta while the others are at the next head's.
 template <typename T>
 constexpr int kGradBuffers = sizeof(T) == 2 ? 2 : 1;   // fp32 tiles leave no LDS for a second place
 
@@ -743,7 +761,7 @@ struct GradLds {
     T x[kGradBuffers<T>][kTileV], dy[kGradBuffers<T>][kTileV];
     T m[kTileV], r[kTileV];                                // L_ij (C_i . B_j) and R_ij as [j][i]
     T q[sizeof(T) == 2 ? NP * Tile<T, kHeadSlab>::kLd : 8];   // Q rounded, [n][channel]
-    GateLds gates[2];
+    GateLds gates[3];
     GradShares<NP / 16> shares[2];
 };
 
@@ -800,7 +818,6 @@ __global__ __launch_bounds__(512, 2) void head_grad(HeadParams p) {
         const int vcols = p.P - slab * kHeadSlab;
         tx.load(xb + col, p.xt, rows, vcols, slab * kHeadSlab);
         ty.load(dyb + col, dyt, rows, vcols, slab * kHeadSlab);
-        dl = gate_load<T>(p, bi, h, ck);
     };
     auto state_at = [&](int h, int slab) {
         return (((bi * p.H + h) * p.slabs + slab) * p.chunks + ck) * (NP * 64);
@@ -814,8 +831,18 @@ __global__ __launch_bounds__(512, 2) void head_grad(HeadParams p) {
             qv[kk] = floats4_2(p.chunk_q + at + 512 * kk, p.chunk_q + at + 512 * kk + 64);
         }
     };
+    constexpr int kGateWave = 1, kFinishWave = 3;
+    auto put_gates = [&](int it, int h, int lane) {
+        lds.gates[it % 3].put(make_gate(Raw<T>::f(dl), p.bias ? p.bias[h] : 0.0f, a2_from_alog(p.A_log[h]), p.softplus,
+                                        lane < rows));
+    };
     fetch(h_first, 0);
     fetch_states(h_first, 0);
+    if (wave == kGateWave) {
+        dl = gate_load<T>(p, bi, h_first, ck);
+        put_gates(0, h_first, lane);
+        dl = gate_load<T>(p, bi, min(p.slabs > 1 ? h_first : h_first + 1, h_last - 1), ck);
+    }
     // What lies above the diagonal is written once.
     for (int i = threadIdx.x; i < Tile<T, kHeadSlab>::kElems; i += 512) lds.m[i] = lds.r[i] = T(0);
     for (int k = 0; k < 2; k++) {
@@ -844,9 +871,8 @@ __global__ __launch_bounds__(512, 2) void head_grad(HeadParams p) {
 #pragma unroll
     for (int k = 0; k < ITW; k++) db[k] = dc[k] = f32x4{0, 0, 0, 0};
 
-    // Sums over the slabs of a head (wave 0, lane t), and what its ddelta takes.
+    // Sums over the slabs of a head (one wave, lane t), and what its ddelta takes.
     float to_sum = 0.0f, from_sum = 0.0f, w_sum = 0.0f, dot_sum = 0.0f, d_sum = 0.0f;
-    constexpr int kGateWave = 4;
     auto finish = [&](const GradShares<NT>& sh, const GateLds& gt, int h, bool done, int lane) {
         const float step = gt.step[lane], raw = gt.raw[lane], decay = gt.in[63];
         float yi = 0.0f, xi = 0.0f, ci = 0.0f;
@@ -893,7 +919,7 @@ __global__ __launch_bounds__(512, 2) void head_grad(HeadParams p) {
         const int buf = it % kGradBuffers<T>;
         T* const x_lds = lds.x[buf];
         T* const dy_lds = lds.dy[buf];
-        GateLds& gates = lds.gates[it & 1];
+        const GateLds& gates = lds.gates[it % 3];
         GradShares<NT>& shares = lds.shares[it & 1];
         const int vcols = p.P - slab * kHeadSlab;
         if (kGradBuffers<T> == 1) barrier_lds();
@@ -903,13 +929,17 @@ __global__ __launch_bounds__(512, 2) void head_grad(HeadParams p) {
         }
         tx.store(x_lds, vcols, 0, rows, slab * kHeadSlab);
         ty.store(dy_lds, vcols, 0, rows, slab * kHeadSlab);
-        if (wave == kGateWave)
-            gates.put(make_gate(Raw<T>::f(dl), p.bias ? p.bias[h] : 0.0f, a2_from_alog(p.A_log[h]), p.softplus,
-                                lane < rows));
         barrier_lds();
         const int next_slab = slab + 1 < p.slabs ? slab + 1 : 0, next_h = next_slab ? h : h + 1;
         if (next_h < h_last) fetch(next_h, next_slab);
-        if (wave == 0 && prev_h >= 0) finish(lds.shares[(it & 1) ^ 1], lds.gates[(it & 1) ^ 1], prev_h, prev_done, lane);
+        // Waves 1 and 3 have no scores: they form the next gates and finish the head before.
+        if (wave == kGateWave && next_h < h_last) {
+            put_gates(it + 1, next_h, lane);
+            const int after = min(next_slab + 1 < p.slabs ? next_h : next_h + 1, h_last - 1);
+            dl = gate_load<T>(p, bi, after, ck);
+        }
+        if (wave == kFinishWave && prev_h >= 0)
+            finish(lds.shares[(it & 1) ^ 1], lds.gates[(it + 2) % 3], prev_h, prev_done, lane);
 
         // Scores.
         {
@@ -1079,9 +1109,9 @@ __global__ __launch_bounds__(512, 2) void head_grad(HeadParams p) {
         slab = next_slab;
     }
     barrier_lds();
-    if (wave == 0) {
-        const int at = ((h_last - h_first) * p.slabs - 1) & 1;
-        finish(lds.shares[at], lds.gates[at], prev_h, true, lane);
+    if (wave == kFinishWave) {
+        const int at = (h_last - h_first) * p.slabs - 1;
+        finish(lds.shares[at & 1], lds.gates[at % 3], prev_h, true, lane);
     }
 #pragma unroll
     for (int k = 0; k < ITW; k++) {
@@ -1203,7 +1233,8 @@ constexpr size_t head_states_lds() {
 }
 template <typename T, int NP, int JOBS>
 constexpr size_t head_out_lds() {
-    return (2 * Tile<T, NP>::kElems + 2 * JOBS * Tile<T, kHeadSlab>::kElems) * sizeof(T) + JOBS * sizeof(GateLds);
+    return (2 * Tile<T, NP>::kElems + 2 * JOBS * Tile<T, kHeadSlab>::kElems) * sizeof(T) +
+           2 * JOBS * sizeof(GateLds);
 }
 template <typename T, int NP>
 constexpr size_t head_grad_lds() {
