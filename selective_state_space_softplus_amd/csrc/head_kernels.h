@@ -58,7 +58,7 @@ struct Gate {
 __device__ __forceinline__ float c_diff(f32x2 a, f32x2 b) { return (a.x - b.x) + (a.y - b.y); }
 
 // The least log2 of one step's decay: 2^-200 is 0 in fp32, and a finite sum has differences.
-constexpr float kLeastDecay = -200.0f;
+constexpr double kLeastDecay = -200.0;
 
 // delta of this lane's step, as it is in memory; past the sequence's end the last one's.
 template <typename T>
@@ -67,11 +67,19 @@ __device__ __forceinline__ typename Raw<T>::type gate_load(const HeadParams& p, 
     return Raw<T>::load(static_cast<const T*>(p.delta), bi * p.deltab + t * p.deltat + h);
 }
 
-__device__ __forceinline__ Gate make_gate(float delta, float bias, float a2, int use_softplus, bool valid) {
+// A log2(e) with A = -exp(A_log), for make_gate.
+__device__ __forceinline__ double decay_rate(float a_log) { return -double(expf(a_log)) * 1.4426950408889634; }
+
+// One wave does this for 64 steps, so it takes the math library's functions,
+// not the hardware's: an error of A or of a steady step size is the same at
+// every step, and adds up over the steps that a state remembers (1.2e-6 of the
+// last state with the hardware's exponential and logarithm, 2e-7 with these).
+__device__ __forceinline__ Gate make_gate(float delta, float bias, double a2, int use_softplus, bool valid) {
     Gate g;
     g.raw = delta + bias;
-    g.step = valid ? (use_softplus ? softplus(g.raw) : g.raw) : 0.0f;
-    const double c = running_sum(valid ? fmaxf(g.step * a2, kLeastDecay) : 0.0f);
+    const float step = use_softplus ? fmaxf(g.raw, 0.0f) + log1pf(expf(-fabsf(g.raw))) : g.raw;
+    g.step = valid ? step : 0.0f;
+    const double c = running_sum(valid ? fmax(double(g.step) * a2, kLeastDecay) : 0.0);
     g.c.x = float(c);
     g.c.y = float(c - double(g.c.x));
     return g;
@@ -363,7 +371,8 @@ __global__ __launch_bounds__(256, 2) void head_states(HeadParams p) {
     const T* const vb = REV ? static_cast<const T*>(p.dy) + w.bi * p.L * p.H * p.P
                             : static_cast<const T*>(p.x) + w.bi * p.xb;
     const int64_t vt = REV ? int64_t(p.H) * p.P : p.xt;
-    const float a2 = a2_from_alog(p.A_log[gate_head]), bias = p.bias ? p.bias[gate_head] : 0.0f;
+    const double a2 = decay_rate(p.A_log[gate_head]);
+    const float bias = p.bias ? p.bias[gate_head] : 0.0f;
 
     f32x4 acc[JOBS][NP / 16];
     float* const seg_at = p.seg_state + w.state_at(p, NP, p.nseg, w.seg);
@@ -499,7 +508,8 @@ __global__ __launch_bounds__(256, 2) void head_out(HeadParams p) {
     const T* const xb = static_cast<const T*>(p.x) + w.bi * p.xb;
     T* const yb = static_cast<T*>(p.y) + w.bi * p.L * p.H * p.P;
     const int64_t yt = int64_t(p.H) * p.P;
-    const float a2 = a2_from_alog(p.A_log[gate_head]), bias = p.bias ? p.bias[gate_head] : 0.0f;
+    const double a2 = decay_rate(p.A_log[gate_head]);
+    const float bias = p.bias ? p.bias[gate_head] : 0.0f;
     const float skip = p.D[w.my_h];
 
     f32x4 acc[JOBS][NP / 16];
@@ -833,7 +843,7 @@ __global__ __launch_bounds__(512, 2) void head_grad(HeadParams p) {
     };
     constexpr int kGateWave = 1, kFinishWave = 3;
     auto put_gates = [&](int it, int h, int lane) {
-        lds.gates[it % 3].put(make_gate(Raw<T>::f(dl), p.bias ? p.bias[h] : 0.0f, a2_from_alog(p.A_log[h]), p.softplus,
+        lds.gates[it % 3].put(make_gate(Raw<T>::f(dl), p.bias ? p.bias[h] : 0.0f, decay_rate(p.A_log[h]), p.softplus,
                                         lane < rows));
     };
     fetch(h_first, 0);
@@ -895,7 +905,7 @@ __global__ __launch_bounds__(512, 2) void head_grad(HeadParams p) {
         // Sums over steps >= t (a running sum in reverse), and < t.
         const float to = __shfl(running_sum(__shfl(to_sum, 63 - lane)), 63 - lane);
         const float from = dpp<0x138>(running_sum(from_sum));   // wave_shr:1, 0 into lane 0
-        const float a = a2_from_alog(p.A_log[h]) * kLn2;
+        const float a = -expf(p.A_log[h]);
         const float dlog = to + from + decay * dot_sum;
         float dstep = a * dlog + w_sum;   // w_sum lacks the step: it is what it is the gradient of
         if (p.softplus) dstep *= rcp_hw(1.0f + exp2_hw(-raw * kLog2e));
