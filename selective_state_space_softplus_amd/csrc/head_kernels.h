@@ -902,20 +902,21 @@ __global__ __launch_bounds__(512, 2) void head_grad(HeadParams p) {
         from_sum += step * xi;
         w_sum += sh.diag[lane] + ci + xi;
         if (!done) return;
-        // Sums over steps >= t (a running sum in reverse), and < t.
-        const float to = __shfl(running_sum(__shfl(to_sum, 63 - lane)), 63 - lane);
-        const float from = dpp<0x138>(running_sum(from_sum));   // wave_shr:1, 0 into lane 0
+        // Sums over steps >= t (a running sum in reverse), and < t; in 64 bits, as what is left of them after the sums
+        // over time can be a small part.
+        const double to = __shfl(running_sum(double(__shfl(to_sum, 63 - lane))), 63 - lane);
+        const double from = dpp_or_zero<0x138, 0xf>(running_sum(double(from_sum)));   // wave_shr:1
         const float a = -expf(p.A_log[h]);
-        const float dlog = to + from + decay * dot_sum;
-        float dstep = a * dlog + w_sum;   // w_sum lacks the step: it is what it is the gradient of
-        if (p.softplus) dstep *= rcp_hw(1.0f + exp2_hw(-raw * kLog2e));
-        if (lane < rows) static_cast<T*>(p.ddelta)[(bi * p.L + t0 + lane) * p.H + h] = narrow<T>(dstep);
-        const float da = running_sum(lane < rows ? dlog * step * a : 0.0f);
-        const float dbias = running_sum(lane < rows ? dstep : 0.0f);
+        const double dlog = to + from + double(decay) * dot_sum;
+        double dstep = a * dlog + w_sum;   // w_sum lacks the step: it is what it is the gradient of
+        if (p.softplus) dstep *= 1.0f / (1.0f + expf(-raw));
+        if (lane < rows) static_cast<T*>(p.ddelta)[(bi * p.L + t0 + lane) * p.H + h] = narrow<T>(float(dstep));
+        const double da = running_sum(lane < rows ? dlog * step * a : 0.0);
+        const double dbias = running_sum(lane < rows ? dstep : 0.0);
         if (lane == 63) {
             const int64_t at = (bi * p.chunks + ck) * p.H + h, one = p.b * p.chunks * p.H;
-            p.partial[at] = da;
-            p.partial[one + at] = dbias;
+            p.partial[at] = float(da);
+            p.partial[one + at] = float(dbias);
             p.partial[2 * one + at] = d_sum;
         }
         to_sum = from_sum = w_sum = dot_sum = d_sum = 0.0f;
@@ -1156,17 +1157,17 @@ __global__ __launch_bounds__(256) void head_sum_blocks(HeadParams p) {
 // dA_log, ddelta_bias and dD from the chunks' shares: one workgroup per head
 // and output, each thread every 256th chunk, then a tree.
 __global__ __launch_bounds__(256) void head_sum_chunks(HeadParams p) {
-    __shared__ float part[4];
+    __shared__ double part[4];
     const int h = int(blockIdx.x) % p.H, k = int(blockIdx.x) / p.H;
     const int64_t count = p.b * p.chunks;
     const float* const src = p.partial + k * count * p.H + h;
-    float v = 0.0f;
+    double v = 0.0;
     for (int64_t i = threadIdx.x; i < count; i += 256) v += src[i * p.H];
-    v = sum_wave(v);
-    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
-    barrier_lds();
+    v = running_sum(v);
+    if ((threadIdx.x & 63) == 63) part[threadIdx.x >> 6] = v;
+    __syncthreads();
     float* const out = k == 0 ? p.dA_log : k == 1 ? p.dbias : p.dD;
-    if (threadIdx.x == 0 && out) out[h] = (part[0] + part[1]) + (part[2] + part[3]);
+    if (threadIdx.x == 0 && out) out[h] = float((part[0] + part[1]) + (part[2] + part[3]));
 }
 
 // One decode step, bound by the state's one read and one write.  A row (b, h, p)
