@@ -263,7 +263,7 @@ __device__ __forceinline__ void state_store(const f32x4 (&acc)[JOBS][NP / 16], f
 // them (Columns), so that one store is 1 KB in a row, and a lane of the
 // gradients still finds 4 neighbouring channels of its n together.  (Storing
 // [n][channel] instead fills the wave's 63 outstanding accesses and stops it:
-// 203 us against what it takes now, b = 1, L = 16384, H = 80.)
+// 203 us against 181 for the pass over the states at b = 1, L = 16384, H = 80, P = 64, N = 128.)
 __device__ __forceinline__ int tile_at(int n, int pc) {
     return ((n >> 4) * 4 + (pc >> 4)) * 256 + ((pc >> 2 & 3) * 16 + (n & 15)) * 4 + (pc & 3);
 }
@@ -351,6 +351,13 @@ enum class StateMode { Local, Chunks };
 //   Chunks: from seg_state (several segments) or the given end state; the state
 //           at entry to every chunk goes to chunk_s or chunk_q, the adjoint one
 //           past the sequence's start to dh0.
+//
+// A Chunks pass is bound by its stores, 4 NP bytes a channel and chunk: 671 MB
+// in 178 us at b = 1, L = 16384, H = 80, P = 64, N = 128 bf16 (3.8 TB/s, what is
+// read with them another 0.24 GB), 57 us at b = 8, L = 2048, H = 24.  A Local pass
+// reads x and B and computes one product a chunk: 104 and 36 us there, set by
+// the loop's latency, products and vector instructions with two waves on a
+// SIMD.  Two jobs a workgroup share the tile of B and halve its reads from LDS.
 template <typename T, int NP, int JOBS, int PARTS, bool REV, StateMode MODE>
 __global__ __launch_bounds__(256, 2) void head_states(HeadParams p) {
     using M = Mat<T>;
@@ -450,7 +457,8 @@ __global__ __launch_bounds__(256, 2) void head_states(HeadParams p) {
 
 // The segments' states from zero, in place, become the states at the segments'
 // starts (REV: the adjoint states at their ends), walking from the given end
-// state.
+// state.  11 us for 12 segments of 80 (64, 128) states, 25 us for 3 segments of
+// 320: short and serial, so eight segments' loads are under way together.
 template <int NP, bool REV>
 __global__ __launch_bounds__(256) void head_carry(HeadParams p) {
     const int64_t at = int64_t(blockIdx.x) * 256 + threadIdx.x;   // (b, h, slab, n, channel)
@@ -486,7 +494,15 @@ __global__ __launch_bounds__(256) void head_carry(HeadParams p) {
 // weighted for each, go through LDS as the first operand of the product with x;
 // the state, held as the accumulators of the update, is rounded to bf16 in
 // place as the second operand of the readout (its rows n are the product's k:
-// lane group g holds n = 4 g + 0..3 of two 16-row tiles).
+// lane group g holds n = 4 g + 0..3 of two 16-row tiles).  The state never
+// leaves the registers between the segment's ends; x, B, C and y move once.
+//
+// 378 us at b = 4, L = 8192, H = 80, P = 64, N = 128 bf16 (1.8 TB/s), 205 at b = 1, L =
+// 16384, H = 80, G = 8: bound by issue, not by memory.  Vector instructions
+// take 47 % of the SIMDs' cycles and products 24 %, at two waves on a SIMD (the
+// state in accumulators and as three operand parts leaves no registers for a
+// third: held to three it spills and is slower).  One pair a workgroup with
+// three resident was slower too, since B and C are then read from LDS twice as often.
 template <typename T, int NP, int JOBS, int PARTS>
 __global__ __launch_bounds__(256, 2) void head_out(HeadParams p) {
     using M = Mat<T>;
@@ -751,6 +767,12 @@ __global__ __launch_bounds__(256, 2) void head_out(HeadParams p) {
 // 32 rows.  Two barriers a head: x, dy and the gates have two places in LDS,
 // and so have the shares of the sums, which a wave without scores turns into
 // ddelta while the others are at the next head's.
+//
+// 171 us at b = 8, L = 2048, H = 24, P = 64, N = 128 bf16, 634 at b = 1, L = 16384, H = 80, G =
+// 8: the chunk's two fp32 states are most of its 0.57 and 2.0 GB (3.2 TB/s).  Of
+// the cycles, vector instructions take 40 %, LDS reads and writes 32 %, products
+// 11 %; a compute unit holds one workgroup (LDS), so two waves on a SIMD have to
+// cover each other's waits.  Four waves with twice the tiles spilled registers.
 template <typename T>
 constexpr int kGradBuffers = sizeof(T) == 2 ? 2 : 1;   // fp32 tiles leave no LDS for a second place
 
@@ -1173,7 +1195,8 @@ __global__ __launch_bounds__(256) void head_sum_chunks(HeadParams p) {
 // One decode step, bound by the state's one read and one write.  A row (b, h, p)
 // of the state is N consecutive values, taken by LPR lanes of 4 (VEC) or one
 // each; a workgroup takes up to ROWS rows a lane group of one head, all their
-// loads under way together, so that B, C and the decay are formed once.
+// loads under way together, so that B, C and the decay are formed once.  245 us
+// at b = 256, H = 80, P = 64, N = 128 (5.5 TB/s); a call for one token 4 us.
 template <typename T, int LPR, int ROWS, bool VEC>
 __global__ __launch_bounds__(256) void head_step(float* state, const T* x, const T* dt, const float* A_log, const T* B,
                                                  const T* C, const float* D, const float* dt_bias, int use_softplus,

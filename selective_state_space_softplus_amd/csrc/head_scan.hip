@@ -47,9 +47,9 @@ int64_t walkers_of(const Shape& s, int dtype) {
 // Segments of the sequence that are walked over at the same time: as many as
 // make all their workgroups resident at once (two to each of 256 compute
 // units), down to one chunk a segment.  More would start a second, mostly
-// empty round: forward b = 4, L = 8192, H = 80 (160 walkers) takes 632 us with 3
-// segments, 746 with 4, 770 with 1; b = 1, L = 16384, H = 80 (40) 379 us with 12,
-// 408 with 16, 438 with 6; b = 1, L = 777, H = 24 (12) 27 us with 13, 72 with 1.
+// empty round: forward b = 4, L = 8192, H = 80 (160 walkers) takes 594 us with 3
+// segments, 647 with 4, 797 with 1; b = 1, L = 16384, H = 80, G = 8 (40) 341 us with 12,
+// 368 with 16, 415 with 6; b = 1, L = 777, H = 24 (12) 28 us with 13, 45 with 4, 76 with 1.
 // The cost is a first pass over x and B for the states at the segments' starts.
 constexpr int64_t kResident = 512;
 
