@@ -39,6 +39,7 @@ struct HeadParams {
     int softplus;
     float *seg_state;       // (b, H, slabs, nseg, NP, 64): the segments' states
     float *seg_decay;       // (b, H, nseg): log2 of the segments' decays
+    float *seg_q, *seg_q_decay;   // the same of the adjoint states
     float *chunk_s;         // (b, H, slabs, chunks, NP, 64): the state before every chunk
     float *chunk_q;         //                               the adjoint state after every chunk
     float *partial;         // (3, b * chunks, H): a chunk's share of dA_log, dbias, dD
@@ -173,9 +174,10 @@ struct Walk {
     int first, last;             // chunks
     int p0;                      // this wave's first channel in the slab
 
-    __device__ __forceinline__ Walk(const HeadParams& p, int nseg, int first_seg) {
+    // `id` of the `count` workgroups that walk over nseg segments from first_seg on.
+    __device__ __forceinline__ Walk(const HeadParams& p, int nseg, int first_seg, uint32_t id, uint32_t count) {
         const int heads = p.H / p.G, jobs = heads * p.slabs, blocks = (jobs + JOBS - 1) / JOBS;
-        const uint32_t piece = piece_of(blockIdx.x, gridDim.x);
+        const uint32_t piece = piece_of(id, count);
         const int at = int(piece % uint32_t(p.G * blocks));
         const uint32_t rest = piece / uint32_t(p.G * blocks);
         g = at / blocks;
@@ -263,7 +265,7 @@ __device__ __forceinline__ void state_store(const f32x4 (&acc)[JOBS][NP / 16], f
 // them (Columns), so that one store is 1 KB in a row, and a lane of the
 // gradients still finds 4 neighbouring channels of its n together.  (Storing
 // [n][channel] instead fills the wave's 63 outstanding accesses and stops it:
-// 203 us against 181 for the pass over the states at b = 1, L = 16384, H = 80, P = 64, N = 128.)
+// 203 us against 181 for a pass over the states alone at b = 1, L = 16384, H = 80, P = 64, N = 128.)
 __device__ __forceinline__ int tile_at(int n, int pc) {
     return ((n >> 4) * 4 + (pc >> 4)) * 256 + ((pc >> 2 & 3) * 16 + (n & 15)) * 4 + (pc & 3);
 }
@@ -352,24 +354,25 @@ enum class StateMode { Local, Chunks };
 //           at entry to every chunk goes to chunk_s or chunk_q, the adjoint one
 //           past the sequence's start to dh0.
 //
-// A Chunks pass is bound by its stores, 4 NP bytes a channel and chunk: 671 MB
-// in 178 us at b = 1, L = 16384, H = 80, P = 64, N = 128 bf16 (3.8 TB/s, what is
-// read with them another 0.24 GB), 57 us at b = 8, L = 2048, H = 24.  A Local pass
-// reads x and B and computes one product a chunk: 104 and 36 us there, set by
-// the loop's latency, products and vector instructions with two waves on a
-// SIMD.  Two jobs a workgroup share the tile of B and halve its reads from LDS.
+// A Chunks pass is bound by its stores, 4 NP bytes a channel and chunk: 1.34 GB
+// for both directions in 368 us at b = 1, L = 16384, H = 80, P = 64, N = 128 bf16 (3.6
+// TB/s, and another 0.48 GB read), 113 us at b = 8, L = 2048, H = 24.  A Local pass
+// reads x and B (dy and C) and computes one product a chunk: 202 and 54 us for
+// both directions there, set by the loop's latency, products and vector instructions
+// with two waves on a SIMD.  Two jobs a workgroup share the tile of B and halve
+// its reads from LDS.
 template <typename T, int NP, int JOBS, int PARTS, bool REV, StateMode MODE>
-__global__ __launch_bounds__(256, 2) void head_states(HeadParams p) {
+__device__ __forceinline__ void states_walk(const HeadParams& p, float* smem, uint32_t id, uint32_t total_ids) {
     using M = Mat<T>;
     using TileK = Tile<T, NP>;
     using TileV = Tile<T, kHeadSlab>;
-    extern __shared__ __align__(16) float smem[];
     T* const k_lds = reinterpret_cast<T*>(smem);
     T* const v_lds = k_lds + TileK::kElems;
     GateLds* const gates = reinterpret_cast<GateLds*>(v_lds + JOBS * TileV::kElems);
 
     // The last segment of the walk has no Local pass: nothing starts from its state.
-    const Walk<JOBS> w(p, MODE == StateMode::Local ? p.nseg - 1 : p.nseg, MODE == StateMode::Local && REV ? 1 : 0);
+    const Walk<JOBS> w(p, MODE == StateMode::Local ? p.nseg - 1 : p.nseg, MODE == StateMode::Local && REV ? 1 : 0, id,
+                       total_ids);
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int gate_head = w.gate_head();
     const T* const kb = REV ? static_cast<const T*>(p.C) + w.bi * p.Cb + int64_t(w.g) * p.N
@@ -382,7 +385,7 @@ __global__ __launch_bounds__(256, 2) void head_states(HeadParams p) {
     const float bias = p.bias ? p.bias[gate_head] : 0.0f;
 
     f32x4 acc[JOBS][NP / 16];
-    float* const seg_at = p.seg_state + w.state_at(p, NP, p.nseg, w.seg);
+    float* const seg_at = (REV ? p.seg_q : p.seg_state) + w.state_at(p, NP, p.nseg, w.seg);
     if (MODE == StateMode::Chunks && p.nseg > 1) state_load<NP, JOBS, Lie::Columns>(acc, seg_at, w.p0);
     else state_read<NP, JOBS, Lie::Columns>(acc, p, w, MODE == StateMode::Chunks ? (REV ? p.dlast : p.h0) : nullptr);
 
@@ -449,18 +452,37 @@ __global__ __launch_bounds__(256, 2) void head_states(HeadParams p) {
     if (!w.my_alive) return;
     if (MODE == StateMode::Local) {
         state_store<NP, JOBS>(acc, seg_at, w.p0);
-        if (w.my_slab == 0 && lane == 0) p.seg_decay[(w.bi * p.H + w.my_h) * p.nseg + w.seg] = total;
+        if (w.my_slab == 0 && lane == 0)
+            (REV ? p.seg_q_decay : p.seg_decay)[(w.bi * p.H + w.my_h) * p.nseg + w.seg] = total;
     } else if (REV && w.seg == 0 && p.dh0) {
         state_write<NP, JOBS, Lie::Columns>(acc, p, w, p.dh0);
     }
 }
 
+// The first half of the workgroups (all of them with RPARTS 0) takes the states,
+// the other the adjoint states.  At the same time each has half as many and
+// longer segments, so less of the sequence needs a Local pass, and launches are
+// fewer: a training step at b = 8, L = 2048, H = 24 takes 442 us, one direction after
+// the other 466; b = 2, L = 1001, H = 12 fp32 97 and 111.
+template <typename T, int NP, int JOBS, int PARTS, int RPARTS, StateMode MODE>
+__global__ __launch_bounds__(256, 2) void head_states(HeadParams p) {
+    extern __shared__ __align__(16) float smem[];
+    if constexpr (RPARTS == 0) {
+        states_walk<T, NP, JOBS, PARTS, false, MODE>(p, smem, blockIdx.x, gridDim.x);
+    } else {
+        const uint32_t half = gridDim.x / 2;
+        if (blockIdx.x < half) states_walk<T, NP, JOBS, PARTS, false, MODE>(p, smem, blockIdx.x, half);
+        else states_walk<T, NP, JOBS, RPARTS, true, MODE>(p, smem, blockIdx.x - half, half);
+    }
+}
+
 // The segments' states from zero, in place, become the states at the segments'
-// starts (REV: the adjoint states at their ends), walking from the given end
-// state.  11 us for 12 segments of 80 (64, 128) states, 25 us for 3 segments of
+// starts (blockIdx.y 1: the adjoint states at their ends), walking from the given end
+// state.  12 us for 12 segments of 80 (64, 128) states, 25 us for 3 segments of
 // 320: short and serial, so eight segments' loads are under way together.
-template <int NP, bool REV>
+template <int NP>
 __global__ __launch_bounds__(256) void head_carry(HeadParams p) {
+    const bool rev = blockIdx.y != 0;
     const int64_t at = int64_t(blockIdx.x) * 256 + threadIdx.x;   // (b, h, slab, n, channel)
     const int64_t total = p.b * p.H * p.slabs * (NP * 64);
     if (at >= total) return;
@@ -468,20 +490,21 @@ __global__ __launch_bounds__(256) void head_carry(HeadParams p) {
     const int64_t bhs = at / (NP * 64), bh = bhs / p.slabs;
     const int pg = int(bhs % p.slabs) * kHeadSlab + pc;
     const bool inside = pg < p.P && n < p.N;
-    const float* const init = REV ? p.dlast : p.h0;
+    const float* const init = rev ? p.dlast : p.h0;
     float s = init && inside ? init[(bh * p.P + pg) * p.N + n] : 0.0f;
-    float* const states = p.seg_state + bhs * p.nseg * (NP * 64) + (at & (NP * 64 - 1));
+    const float* const decays = (rev ? p.seg_q_decay : p.seg_decay) + bh * p.nseg;
+    float* const states = (rev ? p.seg_q : p.seg_state) + bhs * p.nseg * (NP * 64) + (at & (NP * 64 - 1));
     for (int i0 = 0; i0 < p.nseg; i0 += 8) {   // eight segments' loads at a time
         float local[8], decay[8];
 #pragma unroll
         for (int k = 0; k < 8; k++) {
-            const int i = min(i0 + k, p.nseg - 2), seg = REV ? p.nseg - 1 - i : i;   // the last one has neither
+            const int i = min(i0 + k, p.nseg - 2), seg = rev ? p.nseg - 1 - i : i;   // the last one has neither
             local[k] = states[int64_t(seg) * (NP * 64)];
-            decay[k] = p.seg_decay[bh * p.nseg + seg];
+            decay[k] = decays[seg];
         }
 #pragma unroll
         for (int k = 0; k < 8; k++) {
-            const int i = i0 + k, seg = REV ? p.nseg - 1 - i : i;
+            const int i = i0 + k, seg = rev ? p.nseg - 1 - i : i;
             if (i < p.nseg) states[int64_t(seg) * (NP * 64)] = s;
             s = exp2_hw(decay[k]) * s + local[k];
         }
@@ -516,7 +539,7 @@ __global__ __launch_bounds__(256, 2) void head_out(HeadParams p) {
     T* const m_lds = x_lds + JOBS * TileV::kElems;    // weighted scores [i][j]
     GateLds* const gates = reinterpret_cast<GateLds*>(m_lds + JOBS * TileV::kElems);
 
-    const Walk<JOBS> w(p, p.nseg, 0);
+    const Walk<JOBS> w(p, p.nseg, 0, blockIdx.x, gridDim.x);
     const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
     const int gate_head = w.gate_head();
     const T* const bb = static_cast<const T*>(p.B) + w.bi * p.Bb + int64_t(w.g) * p.N;

@@ -53,13 +53,15 @@ int64_t walkers_of(const Shape& s, int dtype) {
 // The cost is a first pass over x and B for the states at the segments' starts.
 constexpr int64_t kResident = 512;
 
-int64_t segment_chunks(const Shape& s, int dtype) {
-    const int64_t segs = std::max<int64_t>(1, std::min(kResident / walkers_of(s, dtype), s.chunks()));
+int64_t segment_chunks(const Shape& s, int dtype, bool grad) {
+    // The gradients walk over the states and the adjoint states at the same time.
+    const int64_t walkers = walkers_of(s, dtype) * (grad ? 2 : 1);
+    const int64_t segs = std::max<int64_t>(1, std::min(kResident / walkers, s.chunks()));
     return (s.chunks() + segs - 1) / segs;
 }
 
-int64_t segments(const Shape& s, int dtype) {
-    return (s.chunks() + segment_chunks(s, dtype) - 1) / segment_chunks(s, dtype);
+int64_t segments(const Shape& s, int dtype, bool grad) {
+    return (s.chunks() + segment_chunks(s, dtype, grad) - 1) / segment_chunks(s, dtype, grad);
 }
 
 // Heads of a group whose shares of dB and dC one workgroup of the backward
@@ -72,12 +74,12 @@ int64_t heads_per_block(const Shape& s) {
 }
 
 struct Workspace {
-    size_t seg_state, seg_decay, chunk_s, chunk_q, partial, dbc, total;
+    size_t seg_state, seg_decay, seg_q, seg_q_decay, chunk_s, chunk_q, partial, dbc, total;
 };
 
 Workspace layout(const Shape& s, int dtype, bool grad) {
     const size_t np = size_t(padded_state(s.N, grad)) * 64 * sizeof(float);
-    const size_t walks = size_t(s.b * s.H * s.slabs()), nseg = size_t(segments(s, dtype));
+    const size_t walks = size_t(s.b * s.H * s.slabs()), nseg = size_t(segments(s, dtype, grad));
     Workspace w{};
     size_t at = 0;
     auto take = [&](size_t& field, size_t bytes) {
@@ -87,6 +89,8 @@ Workspace layout(const Shape& s, int dtype, bool grad) {
     take(w.seg_state, nseg > 1 ? walks * nseg * np : 0);
     take(w.seg_decay, nseg > 1 ? size_t(s.b * s.H) * nseg * sizeof(float) : 0);
     if (grad) {
+        take(w.seg_q, nseg > 1 ? walks * nseg * np : 0);
+        take(w.seg_q_decay, nseg > 1 ? size_t(s.b * s.H) * nseg * sizeof(float) : 0);
         const int64_t per_group = s.H / s.G, per = heads_per_block(s), blocks = (per_group + per - 1) / per;
         take(w.chunk_s, walks * size_t(s.chunks()) * np);
         take(w.chunk_q, walks * size_t(s.chunks()) * np);
@@ -123,8 +127,8 @@ HeadParams params_of(const Shape& s, const Strides& st, int dtype, void* ws, boo
     p.G = int(s.G);
     p.slabs = int(s.slabs());
     p.chunks = int(s.chunks());
-    p.seg_chunks = int(segment_chunks(s, dtype));
-    p.nseg = int(segments(s, dtype));
+    p.seg_chunks = int(segment_chunks(s, dtype, grad));
+    p.nseg = int(segments(s, dtype, grad));
     p.jobs = int(jobs_of(s, dtype));
     p.xb = st.xb;
     p.xt = st.xt;
@@ -138,6 +142,8 @@ HeadParams params_of(const Shape& s, const Strides& st, int dtype, void* ws, boo
     char* const at = static_cast<char*>(ws);
     p.seg_state = reinterpret_cast<float*>(at + w.seg_state);
     p.seg_decay = reinterpret_cast<float*>(at + w.seg_decay);
+    p.seg_q = reinterpret_cast<float*>(at + w.seg_q);
+    p.seg_q_decay = reinterpret_cast<float*>(at + w.seg_q_decay);
     p.chunk_s = reinterpret_cast<float*>(at + w.chunk_s);
     p.chunk_q = reinterpret_cast<float*>(at + w.chunk_q);
     p.partial = reinterpret_cast<float*>(at + w.partial);
@@ -152,13 +158,14 @@ unsigned walkers(const HeadParams& p, int jobs, int nseg) {
     return unsigned(p.b * nseg * p.G * ((p.H / p.G * p.slabs + jobs - 1) / jobs));
 }
 
-// The states at the segments' starts (REV: the adjoint states at their ends).  The last segment of the walk needs
-// no pass of its own.
-template <typename T, int NP, int JOBS, int PARTS, bool REV>
+// The states at the segments' starts (with RPARTS also the adjoint states at their ends).  The last segment of a
+// walk needs no pass of its own.
+template <typename T, int NP, int JOBS, int PARTS, int RPARTS>
 void carry_segments(const HeadParams& p, hipStream_t st) {
-    ss::head_states<T, NP, JOBS, PARTS, REV, StateMode::Local>
-        <<<walkers(p, JOBS, p.nseg - 1), 256, ss::head_states_lds<T, NP, JOBS>(), st>>>(p);
-    ss::head_carry<NP, REV><<<unsigned(p.b * p.H * p.slabs) * (NP * 64 / 256), 256, 0, st>>>(p);
+    constexpr unsigned walks = RPARTS ? 2 : 1;
+    ss::head_states<T, NP, JOBS, PARTS, RPARTS, StateMode::Local>
+        <<<walks * walkers(p, JOBS, p.nseg - 1), 256, ss::head_states_lds<T, NP, JOBS>(), st>>>(p);
+    ss::head_carry<NP><<<dim3(unsigned(p.b * p.H * p.slabs) * (NP * 64 / 256), walks), 256, 0, st>>>(p);
 }
 
 // Parts of the weighted operand of the states' products (fp32 has it whole): three where the states are an output.
@@ -173,7 +180,7 @@ template <typename T, int NP, int JOBS>
 int run_fwd(const HeadParams& p, hipStream_t st) {
     by_parts<T>(p.last != nullptr, [&](auto parts) {
         constexpr int PARTS = decltype(parts)::value;
-        if (p.nseg > 1) carry_segments<T, NP, JOBS, PARTS, false>(p, st);
+        if (p.nseg > 1) carry_segments<T, NP, JOBS, PARTS, 0>(p, st);
         ss::head_out<T, NP, JOBS, PARTS>
             <<<walkers(p, JOBS, p.nseg), 256, ss::head_out_lds<T, NP, JOBS>(), st>>>(p);
     });
@@ -183,16 +190,11 @@ int run_fwd(const HeadParams& p, hipStream_t st) {
 template <typename T, int NP, int JOBS>
 int run_bwd(HeadParams p, hipStream_t st) {
     static_assert(ss::head_grad_lds<T, NP>() <= 160 * 1024, "LDS of a compute unit");
-    constexpr size_t lds = ss::head_states_lds<T, NP, JOBS>();
-    by_parts<T>(false, [&](auto parts) {
-        constexpr int PARTS = decltype(parts)::value;
-        if (p.nseg > 1) carry_segments<T, NP, JOBS, PARTS, false>(p, st);
-        ss::head_states<T, NP, JOBS, PARTS, false, StateMode::Chunks><<<walkers(p, JOBS, p.nseg), 256, lds, st>>>(p);
-    });
     by_parts<T>(p.dh0 != nullptr, [&](auto parts) {
-        constexpr int PARTS = decltype(parts)::value;
-        if (p.nseg > 1) carry_segments<T, NP, JOBS, PARTS, true>(p, st);
-        ss::head_states<T, NP, JOBS, PARTS, true, StateMode::Chunks><<<walkers(p, JOBS, p.nseg), 256, lds, st>>>(p);
+        constexpr int PARTS = sizeof(T) == 2 ? 2 : 1, RPARTS = decltype(parts)::value;
+        if (p.nseg > 1) carry_segments<T, NP, JOBS, PARTS, RPARTS>(p, st);
+        ss::head_states<T, NP, JOBS, PARTS, RPARTS, StateMode::Chunks>
+            <<<2 * walkers(p, JOBS, p.nseg), 256, ss::head_states_lds<T, NP, JOBS>(), st>>>(p);
     });
     const unsigned grid = unsigned(p.b * p.chunks * p.G * p.blocks);
     ss::head_grad<T, NP><<<grid, 512, ss::head_grad_lds<T, NP>(), st>>>(p);
