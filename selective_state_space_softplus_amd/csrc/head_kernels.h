@@ -37,8 +37,10 @@ struct HeadParams {
     int nseg, seg_chunks;   // segments of the sequence, chunks in each but the last
     int jobs;               // (head, slab) pairs of a walking workgroup
     int softplus;
-    float *seg_state;       // (b, H, slabs, nseg, NP, 64): the segments' states
-    float *seg_decay;       // (b, H, nseg): log2 of the segments' decays
+    int pieces, piece_chunks;   // workgroups of a sequence's first pass, chunks in each
+    int slots;              // pieces of segments that the first pass has, at most
+    float *seg_state;       // (b, H, slabs, slots, NP, 64): their states
+    float *seg_decay;       // (b, H, slots): log2 of their decays
     float *seg_q, *seg_q_decay;   // the same of the adjoint states
     float *chunk_s;         // (b, H, slabs, chunks, NP, 64): the state before every chunk
     float *chunk_q;         //                               the adjoint state after every chunk
@@ -46,6 +48,21 @@ struct HeadParams {
     float *dbc;             // (2, blocks, b, L, G, N): shares of dB and dC by head block
     int blocks, per_block;  // head blocks of a group and heads in each
 };
+
+// The first pass takes the chunks before the last segment (REV: after the first
+// one), cut into pieces without regard to segments: a piece's workgroup stores a
+// state at each segment's bound that it meets, and one at its own end.  Where
+// chunk ck's is:
+template <bool REV>
+__device__ __forceinline__ int slot_of(const HeadParams& p, int ck) {
+    return ck / p.seg_chunks + (REV ? ck - p.seg_chunks : ck) / p.piece_chunks;
+}
+// Where segment seg's starting state (REV: adjoint state at its end) is.
+template <bool REV>
+__device__ __forceinline__ int start_slot(const HeadParams& p, int seg) {
+    if (REV) return seg == 0 ? 0 : slot_of<true>(p, min((seg + 1) * p.seg_chunks, p.chunks) - 1);
+    return slot_of<false>(p, seg * p.seg_chunks);
+}
 
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 
@@ -174,14 +191,15 @@ struct Walk {
     int first, last;             // chunks
     int p0;                      // this wave's first channel in the slab
 
-    // `id` of the `count` workgroups that walk over nseg segments from first_seg on.
-    __device__ __forceinline__ Walk(const HeadParams& p, int nseg, int first_seg, uint32_t id, uint32_t count) {
+    // `id` of the `count` workgroups that walk over nseg segments of `length` chunks from chunk `from` to before `to`.
+    __device__ __forceinline__ Walk(const HeadParams& p, int nseg, int length, int from, int to, uint32_t id,
+                                    uint32_t count) {
         const int heads = p.H / p.G, jobs = heads * p.slabs, blocks = (jobs + JOBS - 1) / JOBS;
         const uint32_t piece = piece_of(id, count);
         const int at = int(piece % uint32_t(p.G * blocks));
         const uint32_t rest = piece / uint32_t(p.G * blocks);
         g = at / blocks;
-        seg = first_seg + int(rest % uint32_t(nseg));
+        seg = int(rest % uint32_t(nseg));
         bi = rest / uint32_t(nseg);
 #pragma unroll
         for (int k = 0; k < JOBS; k++) {
@@ -190,8 +208,8 @@ struct Walk {
             h[k] = g * heads + in / p.slabs;
             slab[k] = in % p.slabs;
         }
-        first = seg * p.seg_chunks;
-        last = int(imin(int64_t(first) + p.seg_chunks, p.chunks)) - 1;
+        first = from + seg * length;
+        last = min(first + length, to) - 1;
         const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
         job = wave * JOBS / 4;
         p0 = wave % (4 / JOBS) * kCols;
@@ -371,8 +389,11 @@ __device__ __forceinline__ void states_walk(const HeadParams& p, float* smem, ui
     GateLds* const gates = reinterpret_cast<GateLds*>(v_lds + JOBS * TileV::kElems);
 
     // The last segment of the walk has no Local pass: nothing starts from its state.
-    const Walk<JOBS> w(p, MODE == StateMode::Local ? p.nseg - 1 : p.nseg, MODE == StateMode::Local && REV ? 1 : 0, id,
+    constexpr bool LOCAL = MODE == StateMode::Local;
+    const Walk<JOBS> w(p, LOCAL ? p.pieces : p.nseg, LOCAL ? p.piece_chunks : p.seg_chunks,
+                       LOCAL && REV ? p.seg_chunks : 0, LOCAL && !REV ? (p.nseg - 1) * p.seg_chunks : p.chunks, id,
                        total_ids);
+    if (LOCAL && w.last < w.first) return;   // a short last segment can leave the last piece nothing
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int gate_head = w.gate_head();
     const T* const kb = REV ? static_cast<const T*>(p.C) + w.bi * p.Cb + int64_t(w.g) * p.N
@@ -385,8 +406,10 @@ __device__ __forceinline__ void states_walk(const HeadParams& p, float* smem, ui
     const float bias = p.bias ? p.bias[gate_head] : 0.0f;
 
     f32x4 acc[JOBS][NP / 16];
-    float* const seg_at = (REV ? p.seg_q : p.seg_state) + w.state_at(p, NP, p.nseg, w.seg);
-    if (MODE == StateMode::Chunks && p.nseg > 1) state_load<NP, JOBS, Lie::Columns>(acc, seg_at, w.p0);
+    float* const seg_states = REV ? p.seg_q : p.seg_state;
+    if (MODE == StateMode::Chunks && p.nseg > 1)
+        state_load<NP, JOBS, Lie::Columns>(
+            acc, seg_states + w.state_at(p, NP, p.slots, start_slot<REV>(p, w.seg)), w.p0);
     else state_read<NP, JOBS, Lie::Columns>(acc, p, w, MODE == StateMode::Chunks ? (REV ? p.dlast : p.h0) : nullptr);
 
     TileK tk;
@@ -448,15 +471,21 @@ __device__ __forceinline__ void states_walk(const HeadParams& p, float* smem, ui
         total += cq;
         state_update<T, NP, JOBS, PARTS, Lie::Columns>(acc, exp2_hw(cq), k_lds, vf, REV ? gt.in : gt.out, lane);
         if (done) it++;
+        if (LOCAL && done && (it == count || (REV ? ck : ck + 1) % p.seg_chunks == 0)) {
+            const int slot = slot_of<REV>(p, ck);
+            if (w.my_alive) {
+                state_store<NP, JOBS>(acc, seg_states + w.state_at(p, NP, p.slots, slot), w.p0);
+                if (w.my_slab == 0 && lane == 0)
+                    (REV ? p.seg_q_decay : p.seg_decay)[(w.bi * p.H + w.my_h) * p.slots + slot] = total;
+            }
+            total = 0.0f;
+#pragma unroll
+            for (int ct = 0; ct < JOBS; ct++)
+#pragma unroll
+                for (int nt = 0; nt < NP / 16; nt++) acc[ct][nt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        }
     }
-    if (!w.my_alive) return;
-    if (MODE == StateMode::Local) {
-        state_store<NP, JOBS>(acc, seg_at, w.p0);
-        if (w.my_slab == 0 && lane == 0)
-            (REV ? p.seg_q_decay : p.seg_decay)[(w.bi * p.H + w.my_h) * p.nseg + w.seg] = total;
-    } else if (REV && w.seg == 0 && p.dh0) {
-        state_write<NP, JOBS, Lie::Columns>(acc, p, w, p.dh0);
-    }
+    if (!LOCAL && REV && w.seg == 0 && p.dh0 && w.my_alive) state_write<NP, JOBS, Lie::Columns>(acc, p, w, p.dh0);
 }
 
 // The first half of the workgroups (all of them with RPARTS 0) takes the states,
@@ -476,13 +505,12 @@ __global__ __launch_bounds__(256, 2) void head_states(HeadParams p) {
     }
 }
 
-// The segments' states from zero, in place, become the states at the segments'
+// The states of the first pass become, in place, the states at the segments'
 // starts (blockIdx.y 1: the adjoint states at their ends), walking from the given end
 // state.  12 us for 12 segments of 80 (64, 128) states, 25 us for 3 segments of
 // 320: short and serial, so eight segments' loads are under way together.
-template <int NP>
-__global__ __launch_bounds__(256) void head_carry(HeadParams p) {
-    const bool rev = blockIdx.y != 0;
+template <int NP, bool REV>
+__device__ __forceinline__ void carry_walk(const HeadParams& p) {
     const int64_t at = int64_t(blockIdx.x) * 256 + threadIdx.x;   // (b, h, slab, n, channel)
     const int64_t total = p.b * p.H * p.slabs * (NP * 64);
     if (at >= total) return;
@@ -490,25 +518,58 @@ __global__ __launch_bounds__(256) void head_carry(HeadParams p) {
     const int64_t bhs = at / (NP * 64), bh = bhs / p.slabs;
     const int pg = int(bhs % p.slabs) * kHeadSlab + pc;
     const bool inside = pg < p.P && n < p.N;
-    const float* const init = rev ? p.dlast : p.h0;
+    const float* const init = REV ? p.dlast : p.h0;
     float s = init && inside ? init[(bh * p.P + pg) * p.N + n] : 0.0f;
-    const float* const decays = (rev ? p.seg_q_decay : p.seg_decay) + bh * p.nseg;
-    float* const states = (rev ? p.seg_q : p.seg_state) + bhs * p.nseg * (NP * 64) + (at & (NP * 64 - 1));
-    for (int i0 = 0; i0 < p.nseg; i0 += 8) {   // eight segments' loads at a time
+    const float* const decays = (REV ? p.seg_q_decay : p.seg_decay) + bh * p.slots;
+    float* const states = (REV ? p.seg_q : p.seg_state) + bhs * p.slots * (NP * 64) + (at & (NP * 64 - 1));
+    // From bound to bound: the segment, the piece, and where the walk leaves each.
+    const int end = REV ? p.seg_chunks : (p.nseg - 1) * p.seg_chunks;
+    int ck = REV ? p.chunks : 0, seg = REV ? p.nseg - 1 : 0;
+    int piece = REV ? (p.chunks - 1 - end) / p.piece_chunks : 0;
+    int seg_to = REV ? seg * p.seg_chunks : p.seg_chunks;
+    int piece_to = REV ? end + piece * p.piece_chunks : p.piece_chunks;
+    bool starts = true;
+    while (ck != end) {   // eight slots' loads at a time
         float local[8], decay[8];
+        int slot[8], count = 0;
+        bool first[8];
 #pragma unroll
         for (int k = 0; k < 8; k++) {
-            const int i = min(i0 + k, p.nseg - 2), seg = rev ? p.nseg - 1 - i : i;   // the last one has neither
-            local[k] = states[int64_t(seg) * (NP * 64)];
-            decay[k] = decays[seg];
+            slot[k] = 0;
+            first[k] = false;
+            local[k] = decay[k] = 0.0f;
+            if (ck != end) {
+                slot[k] = seg + piece;
+                first[k] = starts;
+                local[k] = states[int64_t(slot[k]) * (NP * 64)];
+                decay[k] = decays[slot[k]];
+                count = k + 1;
+                ck = REV ? max(seg_to, piece_to) : min(min(seg_to, piece_to), end);
+                starts = ck == seg_to;
+                if (ck == piece_to) {
+                    piece += REV ? -1 : 1;
+                    piece_to += REV ? -p.piece_chunks : p.piece_chunks;
+                }
+                if (starts) {
+                    seg += REV ? -1 : 1;
+                    seg_to += REV ? -p.seg_chunks : p.seg_chunks;
+                }
+            }
         }
 #pragma unroll
-        for (int k = 0; k < 8; k++) {
-            const int i = i0 + k, seg = rev ? p.nseg - 1 - i : i;
-            if (i < p.nseg) states[int64_t(seg) * (NP * 64)] = s;
-            s = exp2_hw(decay[k]) * s + local[k];
-        }
+        for (int k = 0; k < 8; k++)
+            if (k < count) {
+                if (first[k]) states[int64_t(slot[k]) * (NP * 64)] = s;
+                s = exp2_hw(decay[k]) * s + local[k];
+            }
     }
+    states[int64_t(start_slot<REV>(p, REV ? 0 : p.nseg - 1)) * (NP * 64)] = s;
+}
+
+template <int NP>
+__global__ __launch_bounds__(256) void head_carry(HeadParams p) {
+    if (blockIdx.y == 0) carry_walk<NP, false>(p);
+    else carry_walk<NP, true>(p);
 }
 
 // The outputs of a segment, and the last state from the last one.
@@ -539,7 +600,7 @@ __global__ __launch_bounds__(256, 2) void head_out(HeadParams p) {
     T* const m_lds = x_lds + JOBS * TileV::kElems;    // weighted scores [i][j]
     GateLds* const gates = reinterpret_cast<GateLds*>(m_lds + JOBS * TileV::kElems);
 
-    const Walk<JOBS> w(p, p.nseg, 0, blockIdx.x, gridDim.x);
+    const Walk<JOBS> w(p, p.nseg, p.seg_chunks, 0, p.chunks, blockIdx.x, gridDim.x);
     const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
     const int gate_head = w.gate_head();
     const T* const bb = static_cast<const T*>(p.B) + w.bi * p.Bb + int64_t(w.g) * p.N;
@@ -552,7 +613,8 @@ __global__ __launch_bounds__(256, 2) void head_out(HeadParams p) {
     const float skip = p.D[w.my_h];
 
     f32x4 acc[JOBS][NP / 16];
-    if (p.nseg > 1) state_load<NP, JOBS, Lie::Rows>(acc, p.seg_state + w.state_at(p, NP, p.nseg, w.seg), w.p0);
+    if (p.nseg > 1)
+        state_load<NP, JOBS, Lie::Rows>(acc, p.seg_state + w.state_at(p, NP, p.slots, start_slot<false>(p, w.seg)), w.p0);
     else state_read<NP, JOBS, Lie::Rows>(acc, p, w, p.h0);
 
     TileK tb, tc;
