@@ -74,14 +74,14 @@ int64_t heads_per_block(const Shape& s) {
 }
 
 // Chunks of a piece of the first pass: as many pieces as are resident at once, whatever the segments' bounds, where
-// that makes them shorter than segments by a quarter; a bound more is a state more to store and to carry.  Forward b =
+// that makes them shorter than segments by an eighth; a bound more is a state more to store and to carry.  Forward b =
 // 4, L = 8192, H = 80: 3 pieces of 29 chunks 145 us, two segments of 43 195.  Gradients b = 1, L = 16384, H = 80, G =
-// 8: 6 pieces of 36 chunks save 20 us against 5 segments of 43, and the carry takes 14 more.
+// 8: 6 pieces of 36 chunks 154 us and the carry 17, 5 segments of 43 174 and 14.
 int64_t piece_chunks(const Shape& s, int dtype, bool grad) {
     const int64_t segment = segment_chunks(s, dtype, grad), all = (segments(s, dtype, grad) - 1) * segment;
     const int64_t pieces = std::max<int64_t>(1, std::min(kResident / (walkers_of(s, dtype) * (grad ? 2 : 1)), all));
     const int64_t piece = std::max<int64_t>(1, (all + pieces - 1) / pieces);
-    return 4 * piece <= 3 * segment ? piece : segment;
+    return 8 * piece <= 7 * segment ? piece : segment;
 }
 
 int64_t pieces(const Shape& s, int dtype, bool grad) {
