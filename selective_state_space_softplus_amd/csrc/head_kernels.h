@@ -367,7 +367,7 @@ enum class StateMode { Local, Chunks };
 // States over the sequence.
 //   REV false: S over chunks in order, from x and B weighted by exp(c_63 - c_j) s_j.
 //   REV true:  the adjoint state Q backwards, Q = exp(c_63) Q' + sum_i exp(c_i) dy_i C_i^T.
-//   Local:  a segment's state from zero, to seg_state, and its decay to seg_decay.
+//   Local:  the states of a piece from zero, to seg_state, and their decays to seg_decay.
 //   Chunks: from seg_state (several segments) or the given end state; the state
 //           at entry to every chunk goes to chunk_s or chunk_q, the adjoint one
 //           past the sequence's start to dh0.
@@ -375,7 +375,7 @@ enum class StateMode { Local, Chunks };
 // A Chunks pass is bound by its stores, 4 NP bytes a channel and chunk: 1.34 GB
 // for both directions in 368 us at b = 1, L = 16384, H = 80, P = 64, N = 128 bf16 (3.6
 // TB/s, and another 0.48 GB read), 113 us at b = 8, L = 2048, H = 24.  A Local pass
-// reads x and B (dy and C) and computes one product a chunk: 202 and 54 us for
+// reads x and B (dy and C) and computes one product a chunk: 185 and 40 us for
 // both directions there, set by the loop's latency, products and vector instructions
 // with two waves on a SIMD.  Two jobs a workgroup share the tile of B and halve
 // its reads from LDS.
@@ -491,8 +491,8 @@ __device__ __forceinline__ void states_walk(const HeadParams& p, float* smem, ui
 // The first half of the workgroups (all of them with RPARTS 0) takes the states,
 // the other the adjoint states.  At the same time each has half as many and
 // longer segments, so less of the sequence needs a Local pass, and launches are
-// fewer: a training step at b = 8, L = 2048, H = 24 takes 442 us, one direction after
-// the other 466; b = 2, L = 1001, H = 12 fp32 97 and 111.
+// fewer: a training step at b = 8, L = 2048, H = 24 took 442 us where one direction after
+// the other took 466; b = 2, L = 1001, H = 12 fp32 97 and 111.
 template <typename T, int NP, int JOBS, int PARTS, int RPARTS, StateMode MODE>
 __global__ __launch_bounds__(256, 2) void head_states(HeadParams p) {
     extern __shared__ __align__(16) float smem[];
@@ -507,8 +507,8 @@ __global__ __launch_bounds__(256, 2) void head_states(HeadParams p) {
 
 // The states of the first pass become, in place, the states at the segments'
 // starts (blockIdx.y 1: the adjoint states at their ends), walking from the given end
-// state.  12 us for 12 segments of 80 (64, 128) states, 25 us for 3 segments of
-// 320: short and serial, so eight segments' loads are under way together.
+// state.  12 us for 12 segments of 80 (64, 128) states, 26 us for 3 segments of
+// 320: short and serial, so eight slots' loads are under way together.
 template <int NP, bool REV>
 __device__ __forceinline__ void carry_walk(const HeadParams& p) {
     const int64_t at = int64_t(blockIdx.x) * 256 + threadIdx.x;   // (b, h, slab, n, channel)

@@ -49,7 +49,8 @@ int64_t walkers_of(const Shape& s, int dtype) {
 // units), down to one chunk a segment.  More would start a second, mostly
 // empty round: forward b = 4, L = 8192, H = 80 (160 walkers) takes 594 us with 3
 // segments, 647 with 4, 797 with 1; b = 1, L = 16384, H = 80, G = 8 (40) 341 us with 12,
-// 368 with 16, 415 with 6; b = 1, L = 777, H = 24 (12) 28 us with 13, 45 with 4, 76 with 1.
+// 368 with 16, 415 with 6; b = 1, L = 777, H = 24 (12) 28 us with 13, 45 with 4, 76 with 1
+// (the first pass by whole segments in all of these).
 // The cost is a first pass over x and B for the states at the segments' starts.
 constexpr int64_t kResident = 512;
 
