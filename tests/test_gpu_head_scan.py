@@ -159,6 +159,29 @@ def test_non_finite_inputs_stay_causal(ss, dtype, bad):
             assert not torch.isfinite(y[:, at, 0].float()).any()
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_non_finite_x_across_segments(ss, dtype):
+    """The same in segments of several chunks: a NaN x in the first step, at a segment's last step and in between
+    reaches its own channel alone, from its step on, and the others keep their values."""
+    say(f"head scan non-finite in long segments {dtype}")
+    t = inputs(4, 827, 40, 9, 16, 2, dtype, seed=21)
+    for at in (0, 319, 500):
+        x = t["x"].clone()
+        x[1, at, 7, 3] = float("nan")
+        y, last = ss.head_scan_fwd(x, t["delta"], t["A_log"], t["B"], t["C"], t["D"], t["bias"],
+                                   initial_state=t["h0"], return_last_state=True)
+        w = {k: ref.wide(t[k]) for k in NAMES}
+        yr, lr = ref.head_scan(*(w[k] for k in NAMES[:6]), w["bias"], True, w["h0"])
+        reached = torch.zeros(y.shape, dtype=torch.bool)
+        reached[1, at:, 7, 3] = True
+        assert torch.equal(torch.isnan(y.float()).cpu(), reached), at
+        assert torch.isnan(last[1, 7, 3]).all() and torch.isnan(last).sum() == 16, at
+        y, last = y.cpu(), last.cpu()
+        assert ref.rel(y[~reached], yr.cpu()[~reached]) < TOL[dtype], at
+        left = ~torch.isnan(last)
+        assert ref.rel(last[left], lr.cpu()[left]) < TOL[F32], at
+
+
 def grads(ss, t, bias=True, softplus=True):
     return ss.head_scan_bwd(t["x"], t["delta"], t["A_log"], t["B"], t["C"], t["D"], t["dy"],
                             delta_bias=t["bias"] if bias else None, delta_softplus=softplus, initial_state=t["h0"],
@@ -201,6 +224,17 @@ def check_bwd(ss, t, dtype, bias=True, softplus=True):
 def test_backward(ss, shape, dtype):
     say(f"head scan bwd {shape} {dtype}")
     check_bwd(ss, inputs(*shape, dtype, seed=1 + sum(shape), state=shape[1] % 2 == 1), dtype)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("shape", [(8, 827, 40, 8, 8, 1), (4, 827, 40, 9, 16, 2), (2, 827, 40, 8, 8, 1),
+                                   (3, 1500, 42, 16, 8, 2), (2, 700, 100, 8, 8, 4)])
+def test_segments_of_several_chunks(ss, shape, dtype):
+    """Many heads: few segments of several chunks each, whose first pass is cut at other bounds than theirs."""
+    say(f"head scan segments {shape} {dtype}")
+    t = inputs(*shape, dtype, seed=sum(shape))
+    check_fwd(ss, t, dtype)
+    check_bwd(ss, t, dtype)
 
 
 def test_backward_views_and_plain_steps(ss):
